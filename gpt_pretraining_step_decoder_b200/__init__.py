@@ -88,6 +88,12 @@ _SIGS = {
     "fp8_quantize_workspace_bytes": [ctypes.POINTER(_SZ)],
     "fp8_quantize": [_P, _I, _LL, _P, _P, _P, _SZ, _P],
     "gptx_gemm_fp8": [_I, _I, _I, _P, _LL, _P, _LL, _P, _P, _I, _P, _LL, _P],
+    "fp8_block_scale_bytes": [_LL, _LL, ctypes.POINTER(_SZ)],
+    "fp8_block_quantize": [_P, _I, _LL, _LL, _LL, _I, _P, _LL, _P, _P, _LL, _P, _P],
+    "gptx_gemm_fp8_block_workspace_bytes": [_I, _I, _I, ctypes.POINTER(_SZ)],
+    "gptx_gemm_fp8_block": [_I, _I, _I, _P, _LL, _P, _P, _LL, _P, _I, _P, _LL, _I, _P, _SZ, _P],
+    "grad_clip_workspace_bytes": [_I, ctypes.POINTER(_SZ)],
+    "grad_clip": [_I, _P, _P, _P, _P, _F, _P, _P, _SZ, _P],
     "trigram_tally_workspace_bytes": [_LL, _I, ctypes.POINTER(_SZ)],
     "trigram_tally": [_P, _I, _I, _I, _ULL, _ULL, _ULL, _LL, _I, _I, _P, _P, _SZ, _P],
     "muon_update_workspace_bytes": [_I, _I, ctypes.POINTER(_SZ)],
@@ -325,6 +331,74 @@ def fp8_quantize(x, dtype, n, q, scale, workspace, ws_bytes, stream=None):
 def gptx_gemm_fp8(M, N, K, A, lda, B, ldb, scale_a, scale_b, out_dtype, C, ldc, stream=None):
     return _check(_lib.gptx_gemm_fp8(M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(scale_a), _ptr(scale_b), out_dtype,
                                      _ptr(C), ldc, _stream(stream)), "gptx_gemm_fp8")
+
+
+def fp8_block_scale_bytes(rows, cols):
+    """Bytes of the scales of a [rows, cols] matrix of e4m3 codes."""
+    n = ctypes.c_size_t()
+    _check(_lib.fp8_block_scale_bytes(rows, cols, ctypes.byref(n)), "fp8_block_scale_bytes")
+    return n.value
+
+
+def fp8_block_quantize(x, dtype, rows, cols, ldx, square, q, ldq, scales, qt=None, ldqt=0, scales_t=None,
+                       stream=None):
+    """e4m3 codes and exponent-byte scales of x [rows, cols] (q, scales) and / or
+    of its transpose (qt, scales_t); square: one scale per 128 x 128 block
+    instead of one per 128 elements of a row."""
+    return _check(_lib.fp8_block_quantize(_ptr(x), dtype, rows, cols, ldx, int(bool(square)), _ptr(q), ldq,
+                                          _ptr(scales), _ptr(qt), ldqt, _ptr(scales_t), _stream(stream)),
+                  "fp8_block_quantize")
+
+
+def fp8_block_scales(scales, rows, cols):
+    """The stored scales of a [rows, cols] matrix as a plain uint8 tensor
+    [rows, ceil(cols / 128)] of exponent bytes (a scale is 2^(byte - 127))."""
+    ra, ga, groups = -(-rows // 128), -(-cols // 512), -(-cols // 128)
+    return scales.view(ga, ra, 32, 4, 4).permute(1, 3, 2, 0, 4).reshape(ra * 128, ga * 4)[:rows, :groups]
+
+
+def gptx_gemm_fp8_block_workspace_bytes(M, N, K):
+    n = ctypes.c_size_t()
+    _check(_lib.gptx_gemm_fp8_block_workspace_bytes(M, N, K, ctypes.byref(n)), "gptx_gemm_fp8_block_workspace_bytes")
+    return n.value
+
+
+def gptx_gemm_fp8_block(M, N, K, A, lda, scales_a, B, ldb, scales_b, out_dtype, C, ldc, beta=0, workspace=None,
+                        ws_bytes=0, stream=None):
+    """C [M, N] (+)= A B^T of two matrices quantized by fp8_block_quantize."""
+    return _check(_lib.gptx_gemm_fp8_block(M, N, K, _ptr(A), lda, _ptr(scales_a), _ptr(B), ldb, _ptr(scales_b),
+                                           out_dtype, _ptr(C), ldc, int(beta), _ptr(workspace), ws_bytes,
+                                           _stream(stream)), "gptx_gemm_fp8_block")
+
+
+def grad_clip_workspace_bytes(n):
+    b = ctypes.c_size_t()
+    _check(_lib.grad_clip_workspace_bytes(n, ctypes.byref(b)), "grad_clip_workspace_bytes")
+    return b.value
+
+
+def grad_clip(grads, outs, max_norm, norm_out, workspace, ws_bytes, stream=None):
+    """Global L2 norm of a list of contiguous fp32 / bf16 CUDA tensors into
+    norm_out (device float, or None), and the tensors scaled by min(1, max_norm /
+    (norm + 1e-6)): in place (outs None) or into the tensors of outs, which
+    have the same sizes and types.  max_norm = 0: no scaling."""
+    import torch
+    n = len(grads)
+    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+    for i, t in enumerate(grads):
+        o = t if outs is None else outs[i]
+        if t.dtype not in codes or not t.is_contiguous():
+            raise ValueError(f"grad_clip: tensor {i}: a contiguous fp32 or bf16 tensor is wanted")
+        if o is not t and (o.dtype != t.dtype or o.numel() != t.numel() or not o.is_contiguous()):
+            raise ValueError(f"grad_clip: output {i} differs from its tensor in type or size, or is not contiguous")
+    if outs is not None and len(outs) != n:
+        raise ValueError("grad_clip: as many outputs as tensors are wanted")
+    ptrs = (_P * n)(*[t.data_ptr() for t in grads])
+    out_ptrs = None if outs is None else (_P * n)(*[t.data_ptr() for t in outs])
+    sizes = (_LL * n)(*[t.numel() for t in grads])
+    dtypes = (_I * n)(*[codes[t.dtype] for t in grads])
+    return _check(_lib.grad_clip(n, ptrs, out_ptrs, sizes, dtypes, float(max_norm), _ptr(norm_out), _ptr(workspace),
+                                 ws_bytes, _stream(stream)), "grad_clip")
 
 
 def gptx_set_gemm_cta_pairs(on):

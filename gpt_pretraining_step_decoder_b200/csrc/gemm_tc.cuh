@@ -37,7 +37,23 @@
 // instruction): a k-block is still one 128-byte swizzle row per operand row,
 // now 128 elements, so the stage layout, the descriptors and the epilogues are
 // those of the bf16 form; the epilogue multiplies by the two operands' scales
-// (device scalars).  K-major operands only.  K-major and MN-major operands are both read straight from their
+// (device scalars).  K-major operands only.
+//
+// F8 = 2 takes e4m3 operands with one power-of-two scale per row and 128
+// elements of K (kind::mxf8f6f4.block_scale, an exponent byte each).  The
+// instruction wants a scale byte per 32 elements, four of them packed in a
+// 32-bit tensor-memory word, and picks the byte by an id in its descriptor.
+// Here the four bytes of a word are four consecutive 128-element groups, and
+// all four products of a k-block use the same id: one 512-byte atom (128 rows
+// x 4 groups, stored in the order tcgen05.cp reads) serves four k-blocks.  The
+// producer loads the atoms with every fourth k-block, the MMA warp copies them
+// to tensor memory ahead of that block's products (copies and products of one
+// thread execute in order), and the accumulator comes out fully scaled, so the
+// mainloop and the epilogues are those of the unscaled form.  Tiles are 192 or
+// 128 columns wide: two 256-column accumulators would leave no tensor memory
+// for the scales.
+//
+// K-major and MN-major operands are both read straight from their
 // row-major buffers (the UMMA descriptor's major-ness bit), so forward,
 // data-gradient and weight-gradient products need no transposed copies.
 // Split-K writes fp32 partials that a second kernel sums in split order
@@ -83,19 +99,25 @@ template <int KM> struct KmHeavy {
 // BN = 128, 192 or 256 (192 only with fp32 outputs: 96 columns per epilogue
 // warp = three 32-column fp32 blocks); the ring takes what shared memory has
 // left after the epilogue's buffers, at most 6 stages.
-template <int BN, int HEAVY, int CG = 1> struct Cfg {
+// SF = 1 adds a slot of scale atoms to every stage (one of A, BN / 128 rounded
+// up of B) and takes all of TMEM (the scales live behind the accumulators).
+template <int BN, int HEAVY, int CG = 1, int SF = 0> struct Cfg {
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_ROWS = BN / CG;               // B rows this CTA loads per k-block
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int TMEM_COLS = 2 * BN <= 256 ? 256 : 512;  // two accumulators, power of two
+  static constexpr int TMEM_COLS = (2 * BN <= 256 && !SF) ? 256 : 512;  // two accumulators, power of two
+  static constexpr int SFB_ATOMS = SF ? (BN + 127) / 128 : 0;
+  static constexpr int SF_BYTES = SF ? 512 * (1 + SFB_ATOMS) : 0;
+  static_assert(!SF || 2 * BN + 2 * 4 * (1 + SFB_ATOMS) <= 512, "accumulators and scales share TMEM");
   static constexpr int NSTG = HEAVY ? 0 : 1;           // staging blocks per epilogue warp
   static constexpr int NAUX = 2;                       // activation blocks per epilogue warp (ReLU^2 bwd)
   static constexpr int AUX = HEAVY ? NAUX * 32 * 128 : 0;  // activation bytes per epilogue warp
   static constexpr int FIXED = EPI_WARPS * (NSTG * 32 * 128 + AUX) + 1024 /*align*/ + 512 /*barriers*/ +
                                512 /*RoPE turns*/;
-  static constexpr int STAGES = (232448 - FIXED) / STAGE_BYTES > 6 ? 6 : (232448 - FIXED) / STAGE_BYTES;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + FIXED;
+  static constexpr int FIT = (232448 - FIXED) / (STAGE_BYTES + SF_BYTES);
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
+  static constexpr int SMEM_BYTES = STAGES * (STAGE_BYTES + SF_BYTES) + FIXED;
 };
 
 struct Params {
@@ -108,6 +130,10 @@ struct Params {
   GemmEpilogue epi;
   float* partial;  // splits > 1: fp32 [splits, M, N]
   unsigned* err;
+  // F8 = 2: scale atoms of A and B as [k-quads * row atoms, 128 words], and the
+  // row atoms per k-quad
+  CUtensorMap tm_sfa, tm_sfb;
+  int a_atoms, b_atoms;
 };
 
 // ------------------------------------------------------------------ PTX helpers
@@ -314,6 +340,32 @@ __device__ __forceinline__ void tc_mma_ts_w(uint32_t d_tmem, uint32_t a_tmem, ui
                : "memory");
 }
 #undef TC_ELECT_ISSUE
+// block-scaled e4m3 products (scales from tensor memory), warp-issued
+#define TC_MMA_SCALED(cg)                                                                                    \
+  asm volatile("{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"           \
+               "@e tcgen05.mma.cta_group::" cg                                                               \
+               ".kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem), \
+               "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)                       \
+               : "memory")
+template <int CG>
+__device__ __forceinline__ void tc_mma_scaled_w(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate, uint32_t sfa, uint32_t sfb) {
+  if constexpr (CG == 2) TC_MMA_SCALED("2");
+  else TC_MMA_SCALED("1");
+}
+#undef TC_MMA_SCALED
+// one 512-byte scale atom from shared memory (32 rows of 16 bytes) to four
+// tensor-memory columns, repeated in the four lane quarters; of a pair, each
+// CTA copies from its own shared memory to its own tensor memory
+template <int CG>
+__device__ __forceinline__ void tc_copy_scales_w(uint32_t tmem, uint64_t desc) {
+  if constexpr (CG == 2)
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc) : "memory");
+  else
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(tmem), "l"(desc) : "memory");
+}
 __device__ __forceinline__ void tc_commit_w(uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
@@ -351,6 +403,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
          ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Descriptor of a scale atom: unswizzled, 8-row core matrices 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
 }
 
 // Load one operand tile (rows x BK) of the k-block `kb` into `dst`.
@@ -497,6 +554,8 @@ __device__ __forceinline__ void mulsub2(float& y0, float& y1, float p0, float p1
       : "=f"(y0), "=f"(y1)
       : "f"(x0), "f"(x1), "f"(d0), "f"(d1), "f"(p0), "f"(p1));
 }
+// the same for 64-byte rows (64-byte swizzle)
+__device__ __forceinline__ uint32_t swz64(int r, int j) { return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)); }
 __device__ __forceinline__ uint32_t swz128(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
 // cos and sin of the RoPE angle t theta_f from the frequency's turns per
@@ -516,9 +575,9 @@ template <int BN, int KM, typename act_t, int CG, int F8 = 0, bool B3 = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmAux,
-                   const Params p) {
+                   const __grid_constant__ Params p) {
   pdl_wait();     // the previous kernel in the stream has completed (programmatic launch)
-  using C = Cfg<BN, KmHeavy<KM>::value, CG>;
+  using C = Cfg<BN, KmHeavy<KM>::value, CG, F8 == 2>;
   static_assert(CG == 1 || CG == 2, "one CTA or a CTA pair per tile");
   constexpr int KE = F8 ? 128 : BK;  // operand elements per 128-byte k-block row
   extern __shared__ uint8_t smem_raw[];
@@ -528,7 +587,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* sB = smem + C::STAGES * C::A_BYTES;
   uint8_t* stg_all = smem + C::STAGES * C::STAGE_BYTES;
   uint8_t* aux_all = stg_all + EPI_WARPS * C::NSTG * STG_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(aux_all + EPI_WARPS * C::AUX);
+  uint8_t* sSF = aux_all + EPI_WARPS * C::AUX;  // scale atoms: per stage A's, then B's
+  uint64_t* full = reinterpret_cast<uint64_t*>(sSF + C::STAGES * C::SF_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
   uint64_t* tempty = tfull + 2;
@@ -600,17 +660,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int kb1 = min(kb0 + p.kb_per_split, p.kb_total);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.err)) { ok = false; break; }
+          // F8 = 2: the scale atoms of four k-blocks travel with the first (a
+          // row atom past the end only scales rows past the end: clamped)
+          const bool sf = F8 == 2 && (kb & 3) == 0;
+          const uint32_t bytes = C::STAGE_BYTES + (sf ? C::SF_BYTES : 0);
           if constexpr (CG == 2) {
             // both CTAs' bytes complete on the even CTA's stage barrier, which
             // that CTA arms for the pair
             const uint32_t bar0 = mapa_shared(smem_u32(&full[stage]), 0);
-            if (rank == 0) mbar_expect_tx(&full[stage], CG * C::STAGE_BYTES);
+            if (rank == 0) mbar_expect_tx(&full[stage], CG * bytes);
             load_operand_pair<B3>(sA + stage * C::A_BYTES, &tmA, bar0, p.a_kmajor, BM, m0, kb * KE, z);
             load_operand_pair<B3>(sB + stage * C::B_BYTES, &tmB, bar0, p.b_kmajor, C::B_ROWS, n0, kb * KE, z);
+            if constexpr (F8 == 2) {
+              if (sf) {
+                uint8_t* s = sSF + stage * C::SF_BYTES;
+                tma_load_2d_pair(s, &p.tm_sfa, bar0, 0, (kb >> 2) * p.a_atoms + min(m0 / BM, p.a_atoms - 1));
+                tma_load_2d_pair(s + 512, &p.tm_sfb, bar0, 0, (kb >> 2) * p.b_atoms + nt * BN / 128);
+              }
+            }
           } else {
-            mbar_expect_tx(&full[stage], C::STAGE_BYTES);
+            mbar_expect_tx(&full[stage], bytes);
             load_operand<B3>(sA + stage * C::A_BYTES, &tmA, &full[stage], p.a_kmajor, BM, m0, kb * KE, z);
             load_operand<B3>(sB + stage * C::B_BYTES, &tmB, &full[stage], p.b_kmajor, BN, n0, kb * KE, z);
+            if constexpr (F8 == 2) {
+              if (sf) {
+                uint8_t* s = sSF + stage * C::SF_BYTES;
+                tma_load_2d(s, &p.tm_sfa, &full[stage], 0, (kb >> 2) * p.a_atoms + min(m0 / BM, p.a_atoms - 1));
+                tma_load_2d(s + 512, &p.tm_sfb, &full[stage], 0, (kb >> 2) * p.b_atoms + nt * BN / 128);
+              }
+            }
           }
           issued[stage] = true;
           issued_phase[stage] = phase;
@@ -634,9 +712,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // ------------------------------------------------------------ MMA issuer
       // the whole warp runs the loop; one elected lane issues (tc_*_w)
       // D fp32; A, B bf16 (kind::f16) or e4m3 (kind::f8f6f4: format code 0)
-      const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(!p.a_kmajor) << 15) |
-                             ((uint32_t)(!p.b_kmajor) << 16) | ((uint32_t)(BN >> 3) << 17) |
+      // block-scaled: bit 23 = exponent-byte scales, bits 4-5 and 29-30 = the
+      // byte of a scale word that B and A use (set per k-block below)
+      const uint32_t idesc = (F8 == 2 ? (1u << 23) : (1u << 4) | ((uint32_t)(!p.a_kmajor) << 15) |
+                                                         ((uint32_t)(!p.b_kmajor) << 16)) |
+                             (F8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(BN >> 3) << 17) |
                              ((uint32_t)((CG * BM) >> 4) << 24);
+      uint32_t sf_buf = 0;  // two sets of scale columns behind the accumulators, used in turn
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -646,6 +728,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int split = (B3 ? t % per_product : t) % p.splits;
         const int kb0 = split * p.kb_per_split;
         const int kb1 = min(kb0 + p.kb_per_split, p.kb_total);
+        // 192-column tiles start in the middle of a 128-row scale atom every other time
+        uint32_t sfb_shift = 0;
+        if constexpr (F8 == 2 && BN % 128 != 0) {
+          int mt, nt;
+          tile_coords(t / p.splits, p, mt, nt);
+          sfb_shift = (uint32_t)(nt * BN % 128) / 32;
+        }
         if (!warp_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
@@ -654,11 +743,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           tc_fence_after();
           const uint32_t a_base = smem_u32(sA + stage * C::A_BYTES);
           const uint32_t b_base = smem_u32(sB + stage * C::B_BYTES);
+          uint32_t sfa = 0, sfb = 0, sid = 0;
+          if constexpr (F8 == 2) {
+            if ((kb & 3) == 0) {
+              sf_buf ^= 1u;
+              const uint32_t t0 = tmem_base + 2 * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
+              const uint32_t s0 = smem_u32(sSF + stage * C::SF_BYTES);
+#pragma unroll
+              for (int a = 0; a < 1 + C::SFB_ATOMS; ++a) tc_copy_scales_w<CG>(t0 + 4 * a, scale_desc(s0 + 512 * a));
+            }
+            sfa = tmem_base + 2 * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
+            sfb = sfa + 4 + sfb_shift;
+            sid = (uint32_t)(kb & 3);
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k) {  // 32 bytes of K per instruction: 16 bf16 or 32 e4m3
             const uint64_t ad = operand_desc(a_base, p.a_kmajor, k), bd = operand_desc(b_base, p.b_kmajor, k);
             const uint32_t acc_in = (kb > kb0 || k > 0) ? 1u : 0u;
-            if constexpr (CG == 2 && F8) tc_mma_pair_f8_w(d_tmem, ad, bd, idesc, acc_in);
+            if constexpr (F8 == 2)
+              tc_mma_scaled_w<CG>(d_tmem, ad, bd, idesc | (sid << 4) | (sid << 29), acc_in, sfa, sfb);
+            else if constexpr (CG == 2 && F8) tc_mma_pair_f8_w(d_tmem, ad, bd, idesc, acc_in);
             else if constexpr (CG == 2) tc_mma_pair_w(d_tmem, ad, bd, idesc, acc_in);
             else if constexpr (F8) tc_mma_f8_w(d_tmem, ad, bd, idesc, acc_in);
             else tc_mma_w(d_tmem, ad, bd, idesc, acc_in);
@@ -687,10 +791,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const GemmEpilogue& e = p.epi;
     // acc scale: alpha times the operands' device scales (the FP8 path), if any
     float ealpha = e.alpha;
-    if constexpr (F8) ealpha *= (e.scale_a ? *e.scale_a : 1.f) * (e.scale_b ? *e.scale_b : 1.f);
+    if constexpr (F8 == 1) ealpha *= (e.scale_a ? *e.scale_a : 1.f) * (e.scale_b ? *e.scale_b : 1.f);
     constexpr bool f32out = KM == K_STORE_F32 || KM == K_REDUCE_F32 || KM == K_PARTIAL;
     constexpr bool has_aux = KM == K_DRELU2 || KM == K_AXPBY;
-    constexpr int CW = f32out ? 32 : 64;  // columns per 128-byte staging row
+    // columns per staging row: 128 bytes, or 64 where a bf16 half tile is no multiple of 64 columns
+    constexpr bool narrow = F8 == 2 && !f32out && HALF % 64 != 0;
+    constexpr int CW = f32out || narrow ? 32 : 64;
     static_assert(!has_aux || HALF / CW <= C::NAUX, "one activation block per column block");
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -949,7 +1055,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < CW / 8; ++j) {
             uint4 o;
             __nv_bfloat162 b0 = __floats2bfloat162_rn(v[8 * j], v[8 * j + 1]);
             __nv_bfloat162 b1 = __floats2bfloat162_rn(v[8 * j + 2], v[8 * j + 3]);
@@ -959,7 +1065,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             o.y = *reinterpret_cast<uint32_t*>(&b1);
             o.z = *reinterpret_cast<uint32_t*>(&b2);
             o.w = *reinterpret_cast<uint32_t*>(&b3);
-            *reinterpret_cast<uint4*>(stg + swz128(lane, j)) = o;
+            *reinterpret_cast<uint4*>(stg + (narrow ? swz64(lane, j) : swz128(lane, j))) = o;
           }
         }
         fence_async_smem();

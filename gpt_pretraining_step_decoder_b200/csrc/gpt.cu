@@ -208,16 +208,24 @@ static int resident_clusters(K* kernel, int smem, int cg) {
   return n;
 }
 
+constexpr int MAX_DEVICES = 128;
+
 template <int BN, int KM, int CG, int F8 = 0, bool B3 = false>
 static int gemm_tc_launch_k(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tcm,
                             const CUtensorMap& taux, const tc::Params& p, cudaStream_t st) {
-  using C = tc::Cfg<BN, tc::KmHeavy<KM>::value, CG>;
+  using C = tc::Cfg<BN, tc::KmHeavy<KM>::value, CG, F8 == 2>;
   static_assert(C::SMEM_BYTES <= 232448, "shared memory budget");
   auto kernel = tc::gemm_tc_kernel<BN, KM, bf16, CG, F8, B3>;
-  static int units = 0;
+  // per device: the shared-memory limit belongs to the kernel on that device
+  static std::atomic<int> device_units[MAX_DEVICES];
+  int dev = 0;
+  CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 0 || dev >= MAX_DEVICES) return fail(GPT_ERR_ARG, "device index %d out of range", dev);
+  int units = device_units[dev].load();
   if (!units) {
     CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES));
     units = resident_clusters(kernel, C::SMEM_BYTES, CG);
+    device_units[dev].store(units);
   }
   const int tiles = p.m_tiles * p.n_tiles * p.splits * p.batch;
   const int grid = CG * (tiles < units ? tiles : units);
@@ -1854,6 +1862,7 @@ extern "C" int ngram_sync_status(void* stream) {
   }
   if (w & GPT_EBIT_INPUT) return fail(GPT_ERR_INPUT, "row or token id out of range");
   if (w & GPT_EBIT_TIMEOUT) return fail(GPT_ERR_TIMEOUT, "a kernel's bounded wait gave up");
+  if (w & GPT_EBIT_NONFINITE) return fail(GPT_ERR_NONFINITE, "loss or gradient norm not finite");
   return GPT_OK;
 }
 
@@ -2142,3 +2151,5 @@ extern "C" int ngram_sparse_update_noalloc(void* table, float* row_state, long l
   if (dev != cur) CUDA_TRY(cudaSetDevice(cur));
   return s;
 }
+
+#include "train_ops.cuh"

@@ -1,0 +1,328 @@
+// train_ops.cuh -- C entry points of the standalone training operators on the
+// caller's tensors: block-scaled FP8 quantization and product, and gradient
+// clipping over many tensors.  Included once, by gpt.cu, whose helpers
+// (status codes, tensor maps, launches, GEMM dispatch) it uses.  Documented in
+// include/gpt.h.
+#pragma once
+#include "clip.cuh"
+#include "fp8_block.cuh"
+
+// ======================================================================== device of a call
+// A call runs on the device of its tensors, made current for the call and
+// restored after; a stream of another device is refused by the launch.  (The
+// stream itself cannot be asked for its device while it is being captured.)
+// Every tensor has to be device memory of that device: a host pointer or
+// another GPU's would fault in the kernel.
+struct DeviceScope {
+  int prev = -1, dev = -1;
+  int enter(const char* fn, const void* p) {
+    CUDA_TRY(cudaGetDevice(&prev));
+    cudaPointerAttributes a;
+    CUDA_TRY(cudaPointerGetAttributes(&a, p));
+    if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
+      return fail(GPT_ERR_ARG, "%s: a tensor is no device memory", fn);
+    dev = a.type == cudaMemoryTypeDevice ? a.device : prev;
+    if (dev != prev) CUDA_TRY(cudaSetDevice(dev));
+    return GPT_OK;
+  }
+  int check(const char* fn, const char* what, const void* p) const {
+    if (!p) return GPT_OK;
+    cudaPointerAttributes a;
+    CUDA_TRY(cudaPointerGetAttributes(&a, p));
+    if (a.type == cudaMemoryTypeManaged) return GPT_OK;
+    if (a.type != cudaMemoryTypeDevice || a.device != dev)
+      return fail(GPT_ERR_ARG, "%s: %s is no memory of device %d", fn, what, dev);
+    return GPT_OK;
+  }
+  ~DeviceScope() {
+    if (dev >= 0 && dev != prev) cudaSetDevice(prev);
+  }
+};
+#define ON_DEVICE_OF(fn, p) \
+  DeviceScope scope_;       \
+  TRY(scope_.enter(fn, p))
+#define CHECK_PTR(fn, p) TRY(scope_.check(fn, #p, p))
+
+static bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+static size_t dtype_size(int dtype) { return dtype == GPT_DTYPE_BF16 ? 2 : 4; }
+
+// ======================================================================== block-scaled FP8
+static long long scale_atoms(long long rows, long long cols) { return cdiv_ll(rows, 128) * cdiv_ll(cols, 512); }
+
+extern "C" int fp8_block_scale_bytes(long long rows, long long cols, size_t* bytes) {
+  if (!bytes || rows < 1 || cols < 1 || rows > (1LL << 31) || cols > (1LL << 31))
+    return fail(GPT_ERR_ARG, "fp8_block_scale_bytes: bad argument");
+  *bytes = (size_t)scale_atoms(rows, cols) * 512;
+  return GPT_OK;
+}
+
+extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long long cols, long long ldx, int square,
+                                  uint8_t* q, long long ldq, uint8_t* scales, uint8_t* qt, long long ldqt,
+                                  uint8_t* scales_t, void* stream) {
+  const char* fn = "fp8_block_quantize";
+  if (!x || rows < 0 || cols < 0 || rows > (1LL << 31) || cols > (1LL << 31) || ldx < cols || (!q && !qt))
+    return fail(GPT_ERR_ARG, "%s: bad argument", fn);
+  if (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16) return fail(GPT_ERR_ARG, "%s: bad dtype", fn);
+  if ((q && (!scales || ldq < cols || ldq % 16 || misaligned(q, 16) || misaligned(scales, 16))) ||
+      (qt && (!scales_t || ldqt < rows || ldqt % 16 || misaligned(qt, 16) || misaligned(scales_t, 16))))
+    return fail(GPT_ERR_ARG, "%s: codes need scales, a row pitch that covers a row in a multiple of 16 bytes, "
+                             "and 16-byte aligned addresses", fn);
+  if (misaligned(x, dtype_size(dtype))) return fail(GPT_ERR_ARG, "%s: x is not aligned to its elements", fn);
+  const long long tiles = cdiv_ll(rows, 128) * cdiv_ll(cols, 128);
+  if (tiles == 0) return GPT_OK;
+  if (tiles > 0x7fffffffLL) return fail(GPT_ERR_ARG, "%s: too many elements", fn);
+  cudaStream_t st = (cudaStream_t)stream;
+  ON_DEVICE_OF(fn, x);
+  CHECK_PTR(fn, q); CHECK_PTR(fn, scales); CHECK_PTR(fn, qt); CHECK_PTR(fn, scales_t);
+  const int vec = !misaligned(x, 16) && (ldx * (long long)dtype_size(dtype)) % 16 == 0;
+  const QuantArgs a{rows, cols, ldx, q, ldq, scales, qt, ldqt, scales_t, square != 0, vec};
+  ++g_launches;
+  if (dtype == GPT_DTYPE_BF16)
+    launch_pdl(fp8_block_quantize_kernel<bf16>, (unsigned)tiles, 256, 0, st, (const bf16*)x, a);
+  else
+    launch_pdl(fp8_block_quantize_kernel<float>, (unsigned)tiles, 256, 0, st, (const float*)x, a);
+  LAUNCH_CHECK();
+  return GPT_OK;
+}
+
+// Tile shape and K split of a block-scaled product: pairs of SMs (256-row
+// tiles) where there is more than one block of 128 rows, and the width (192 or
+// 128 columns) and split with the least estimated time, in SM cycles: whole
+// waves of tiles, each k-block the longer of its MMAs and of its operands' way
+// from L2 (about 64 bytes a cycle and SM), plus the tile's start and epilogue;
+// a split adds its second launch and the partials' way through L2.  K is split in
+// whole scale atoms (4 k-blocks).
+struct F8bPlan { int bn, cg, splits; };
+static F8bPlan f8b_plan(int M, int N, int K) {
+  const int cg = M > 128 && gemm_pairs_enabled() ? 2 : 1;
+  const int quads = cdiv(K, 512), units = device_sms() / cg;
+  F8bPlan best{128, cg, 1};
+  double best_t = 1e300;
+  for (int bn : {192, 128}) {
+    if (bn == 192 && (cg == 1 || N <= 128)) continue;
+    const double kb_cycles = std::max(2.0 * bn, (128 + bn / cg) * 128 / 64.0);
+    const long long tiles = (long long)cdiv(M, 128 * cg) * cdiv(N, bn);
+    for (int s = 1; s <= (N % 4 == 0 && tiles < units ? std::min(32, quads) : 1); ++s) {
+      const int share = cdiv(quads, s);
+      if (cdiv(quads, share) != s) continue;  // the same shares as a smaller split
+      const double waves = (double)((tiles * s + units - 1) / units);
+      const double t = waves * (share * 4 * kb_cycles + 1500.0) + (s > 1 ? 6000.0 + (double)s * M * N * 8 / 5000.0 : 0.0);
+      if (t < best_t) { best = F8bPlan{bn, cg, s}; best_t = t; }
+    }
+  }
+  return best;
+}
+
+template <int BN, int CG>
+static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda, const uint8_t* sa, const uint8_t* B,
+                           long long ldb, const uint8_t* sb, GemmEpilogue e, int splits, float* partial, unsigned* err,
+                           cudaStream_t st) {
+  CUtensorMap ta, tb, tcm;
+  tc::Params p;
+  const uint64_t da[2] = {(uint64_t)K, (uint64_t)M}, la[1] = {(uint64_t)lda};
+  const uint32_t ba[2] = {128, tc::BM};
+  TRY(make_tmap_gen(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, A, da, la, ba));
+  const uint64_t db[2] = {(uint64_t)K, (uint64_t)N}, lb[1] = {(uint64_t)ldb};
+  const uint32_t bb[2] = {128, (uint32_t)(BN / CG)};
+  TRY(make_tmap_gen(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, B, db, lb, bb));
+  const uint64_t dsa[2] = {128, (uint64_t)scale_atoms(M, K)}, dsb[2] = {128, (uint64_t)scale_atoms(N, K)}, ls[1] = {512};
+  const uint32_t bsa[2] = {128, 1}, bsb[2] = {128, (BN + 127) / 128};
+  TRY(make_tmap_gen(&p.tm_sfa, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sa, dsa, ls, bsa, CU_TENSOR_MAP_SWIZZLE_NONE));
+  TRY(make_tmap_gen(&p.tm_sfb, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sb, dsb, ls, bsb, CU_TENSOR_MAP_SWIZZLE_NONE));
+  p.a_atoms = cdiv(M, 128); p.b_atoms = cdiv(N, 128);
+  p.M = M; p.N = N; p.K = K; p.batch = 1;
+  p.a_kmajor = 1; p.b_kmajor = 1;
+  p.m_tiles = cdiv(M, CG * tc::BM);
+  p.n_tiles = cdiv(N, BN);
+  p.group_m = (double)N * K > 32.0 * (1 << 20) ? std::min(p.m_tiles, 16) : 1;
+  p.kb_total = cdiv(K, 128);
+  p.kb_per_split = 4 * cdiv(cdiv(p.kb_total, 4), splits);
+  p.splits = cdiv(p.kb_total, p.kb_per_split);
+  p.epi = e; p.partial = partial; p.err = err;
+  const bool f32 = e.mode != EPI_STORE;
+  if (p.splits > 1) {
+    const uint64_t dims[3] = {(uint64_t)N, (uint64_t)M, (uint64_t)p.splits};
+    const uint64_t str[2] = {(uint64_t)N * 4, (uint64_t)M * N * 4};
+    const uint32_t box[3] = {32, 32, 1};
+    TRY(make_tmap_gen(&tcm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, partial, dims, str, box));
+    TRY((gemm_tc_launch_k<BN, tc::K_PARTIAL, CG, 2>(ta, tb, tcm, tcm, p, st)));
+    const long long total = (long long)M * N;
+    const int blocks = (int)std::min<long long>((total + 255) / 256, 4LL * device_sms());
+    ++g_launches; launch_pdl(splitk_reduce_kernel<bf16>, blocks, 256, 0, st, partial, p.splits, M, N, e);
+    LAUNCH_CHECK();
+    return GPT_OK;
+  }
+  const uint64_t dims[2] = {(uint64_t)N, (uint64_t)M}, str[1] = {(uint64_t)e.ldc * (f32 ? 4 : 2)};
+  // bf16 half tiles of 96 columns go out in 32-column blocks (64-byte rows)
+  constexpr bool narrow = (BN / 2) % 64 != 0;
+  const uint32_t box[2] = {f32 || narrow ? 32u : 64u, 32};
+  TRY(make_tmap_gen(&tcm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, e.C, dims, str, box,
+                    f32 || !narrow ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
+  if (!f32) return gemm_tc_launch_k<BN, tc::K_STORE, CG, 2>(ta, tb, tcm, tcm, p, st);
+  if (e.beta) return gemm_tc_launch_k<BN, tc::K_REDUCE_F32, CG, 2>(ta, tb, tcm, tcm, p, st);
+  return gemm_tc_launch_k<BN, tc::K_STORE_F32, CG, 2>(ta, tb, tcm, tcm, p, st);
+}
+
+extern "C" int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes) {
+  if (!bytes || M < 1 || N < 1 || K < 1) return fail(GPT_ERR_ARG, "gptx_gemm_fp8_block_workspace_bytes: bad argument");
+  const F8bPlan pl = f8b_plan(M, N, K);
+  *bytes = pl.splits > 1 ? (size_t)pl.splits * M * N * 4 : 0;
+  return GPT_OK;
+}
+
+extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long long lda, const uint8_t* scales_a,
+                                   const uint8_t* B, long long ldb, const uint8_t* scales_b, int out_dtype, void* C,
+                                   long long ldc, int beta, void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "gptx_gemm_fp8_block";
+  if (M < 1 || N < 1 || K < 1 || !A || !B || !C || !scales_a || !scales_b || ldc < N || lda < K || ldb < K)
+    return fail(GPT_ERR_ARG, "%s: bad argument", fn);
+  if (out_dtype != GPT_DTYPE_F32 && out_dtype != GPT_DTYPE_BF16) return fail(GPT_ERR_ARG, "%s: bad out_dtype", fn);
+  if (beta && out_dtype != GPT_DTYPE_F32) return fail(GPT_ERR_ARG, "%s: beta needs an fp32 output", fn);
+  if ((lda | ldb) % 16 || (ldc * (long long)dtype_size(out_dtype)) % 16 || misaligned(A, 16) || misaligned(B, 16) ||
+      misaligned(C, 16) || misaligned(scales_a, 16) || misaligned(scales_b, 16))
+    return fail(GPT_ERR_ARG, "%s: addresses and row pitches must be multiples of 16 bytes", fn);
+  cudaStream_t st = (cudaStream_t)stream;
+  const F8bPlan pl = f8b_plan(M, N, K);
+  const size_t need = pl.splits > 1 ? (size_t)pl.splits * M * N * 4 : 0;
+  if (need && (!workspace || ws_bytes < need))
+    return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, need);
+  if (need && misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
+  ON_DEVICE_OF(fn, A);
+  CHECK_PTR(fn, B); CHECK_PTR(fn, C); CHECK_PTR(fn, scales_a); CHECK_PTR(fn, scales_b);
+  if (need) CHECK_PTR(fn, workspace);
+  unsigned* err = nullptr;
+  CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
+  const GemmEpilogue e = epi(out_dtype == GPT_DTYPE_BF16 ? EPI_STORE : EPI_ACCUM_F32, C, ldc, beta != 0);
+  float* part = static_cast<float*>(workspace);
+  if (pl.bn == 192) return gemm_f8b_launch<192, 2>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
+  if (pl.cg == 2) return gemm_f8b_launch<128, 2>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
+  return gemm_f8b_launch<128, 1>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
+}
+
+// ======================================================================== gradient clipping
+extern "C" int grad_clip_workspace_bytes(int n, size_t* bytes) {
+  if (!bytes || n < 0) return fail(GPT_ERR_ARG, "grad_clip_workspace_bytes: bad argument");
+  *bytes = (size_t)std::max(1, cdiv(n, CLIP_MAX_TENSORS)) * CLIP_BLOCKS * sizeof(double);
+  return GPT_OK;
+}
+
+template <int CAP>
+static int clip_fill(ClipTable<CAP>& t, int n, const void* const* grads, void* const* outs, const long long* sizes,
+                     const int* dtypes) {
+  long long pieces = 0;
+  t.n = n;
+  for (int i = 0; i < n; ++i) {
+    const bool lp = dtypes[i] == GPT_DTYPE_BF16;
+    t.g[i] = grads[i];
+    t.out[i] = outs ? outs[i] : const_cast<void*>(grads[i]);
+    t.size_bf16[i] = (unsigned long long)sizes[i] << 1 | (lp ? 1 : 0);
+    t.piece0[i] = (int)pieces;
+    pieces += cdiv_ll(sizes[i], lp ? CLIP_PIECE / 2 : CLIP_PIECE / 4);
+    if (pieces > 0x3fffffffLL) return fail(GPT_ERR_ARG, "grad_clip: too many elements");
+  }
+  t.piece0[n] = (int)pieces;
+  return GPT_OK;
+}
+
+// both passes over all tensors, CAP of them a launch
+template <int CAP>
+static int clip_run(int n, const void* const* grads, void* const* outs, const long long* sizes, const int* dtypes,
+                    float max_norm, float* norm_out, double* part, unsigned* err, cudaStream_t st) {
+  ClipTable<CAP> t;
+  const int launches = std::max(1, cdiv(n, CAP));
+  int parts = 0;
+  for (int pass = 0; pass < 2; ++pass)
+    for (int l = 0; l < launches; ++l) {
+      const int i0 = l * CAP, m = std::min(CAP, n - i0);
+      if (pass == 0 || launches > 1)
+        TRY(clip_fill(t, m, grads + i0, outs ? outs + i0 : nullptr, sizes + i0, dtypes + i0));
+      const int grid = std::max(1, std::min(CLIP_BLOCKS, t.piece0[m]));
+      ++g_launches;
+      if (pass == 0) {
+        launch_pdl(clip_sumsq_kernel<CAP>, grid, CLIP_THREADS, 0, st, t, part + parts);
+        parts += grid;
+      } else {
+        // the norm alone needs no more than the first block
+        const bool scale = outs || max_norm > 0.f;
+        if (!scale && l > 0) break;
+        launch_pdl(clip_scale_kernel<CAP>, scale ? grid : 1, CLIP_THREADS, 0, st, t, (const double*)part, parts, max_norm,
+                   outs ? 0 : 1, l == 0 ? norm_out : nullptr, err);
+      }
+      LAUNCH_CHECK();
+    }
+  return GPT_OK;
+}
+
+// A tensor that overlaps what another one writes (two blocks would scale the
+// same elements, or one would read what the other has scaled), or -1.  `order`:
+// n ints of scratch.
+static int clip_overlap(int n, const void* const* grads, void* const* outs, const long long* sizes, const int* dtypes,
+                        int* order) {
+  auto in0 = [&](int i) { return reinterpret_cast<uintptr_t>(grads[i]); };
+  auto out0 = [&](int i) { return reinterpret_cast<uintptr_t>(outs ? outs[i] : grads[i]); };
+  auto len = [&](int i) { return (uintptr_t)sizes[i] * dtype_size(dtypes[i]); };
+  int m = 0;
+  bool ascending = true;
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] == 0) continue;
+    if (m > 0 && out0(order[m - 1]) > out0(i)) ascending = false;
+    order[m++] = i;
+  }
+  if (!ascending) std::sort(order, order + m, [&](int a, int b) { return out0(a) < out0(b); });
+  for (int k = 1; k < m; ++k)
+    if (out0(order[k - 1]) + len(order[k - 1]) > out0(order[k])) return order[k];
+  if (!outs) return -1;
+  // the outputs are disjoint and sorted: those that an input meets are neighbours
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] == 0) continue;
+    int lo = 0, hi = m;  // first output that ends behind the input's start
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (out0(order[mid]) + len(order[mid]) > in0(i)) hi = mid;
+      else lo = mid + 1;
+    }
+    for (; lo < m && out0(order[lo]) < in0(i) + len(i); ++lo)
+      if (order[lo] != i || out0(i) != in0(i)) return i;
+  }
+  return -1;
+}
+
+extern "C" int grad_clip(int n, const void* const* grads, void* const* outs, const long long* sizes, const int* dtypes,
+                         float max_norm, float* norm_out, void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "grad_clip";
+  if (n < 0 || (n > 0 && (!grads || !sizes || !dtypes)) || !(max_norm >= 0.f))
+    return fail(GPT_ERR_ARG, "%s: bad argument (max_norm >= 0)", fn);
+  size_t need = 0;
+  TRY(grad_clip_workspace_bytes(n, &need));
+  for (int i = 0; i < n; ++i) {
+    if (dtypes[i] != GPT_DTYPE_F32 && dtypes[i] != GPT_DTYPE_BF16) return fail(GPT_ERR_ARG, "%s: tensor %d: bad dtype", fn, i);
+    const size_t es = dtype_size(dtypes[i]);
+    if (sizes[i] < 0 || sizes[i] > (1LL << 46) || (sizes[i] > 0 && (!grads[i] || (outs && !outs[i]))))
+      return fail(GPT_ERR_ARG, "%s: tensor %d: null pointer or bad size", fn, i);
+    if (sizes[i] > 0 && (misaligned(grads[i], es) || (outs && misaligned(outs[i], es))))
+      return fail(GPT_ERR_ARG, "%s: tensor %d is not aligned to its elements", fn, i);
+  }
+  if (!workspace || ws_bytes < need) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, need);
+  if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
+  if (n > 0) {
+    int* order = static_cast<int*>(malloc((size_t)n * sizeof(int)));
+    if (!order) return fail(GPT_ERR_ARG, "%s: out of host memory", fn);
+    const int bad = clip_overlap(n, grads, outs, sizes, dtypes, order);
+    free(order);
+    if (bad >= 0) return fail(GPT_ERR_ARG, "%s: tensor %d overlaps another one that is written", fn, bad);
+  }
+  cudaStream_t st = (cudaStream_t)stream;
+  ON_DEVICE_OF(fn, workspace);
+  CHECK_PTR(fn, norm_out);
+  for (int i = 0; i < n; ++i) {
+    if (sizes[i] == 0) continue;
+    CHECK_PTR(fn, grads[i]);
+    if (outs) CHECK_PTR(fn, outs[i]);
+  }
+  unsigned* err = nullptr;
+  CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
+  double* part = static_cast<double*>(workspace);
+  if (n <= CLIP_FEW_TENSORS)
+    return clip_run<CLIP_FEW_TENSORS>(n, grads, outs, sizes, dtypes, max_norm, norm_out, part, err, st);
+  return clip_run<CLIP_MAX_TENSORS>(n, grads, outs, sizes, dtypes, max_norm, norm_out, part, err, st);
+}

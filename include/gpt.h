@@ -332,8 +332,9 @@ int ngram_sparse_update(void* table, float* row_state, long long n_rows, int d, 
 
 /* Synchronise `stream` and read + clear the standalone operations' device
  * error word (GPT_ERR_INPUT for out-of-range ids, GPT_ERR_TIMEOUT for a bounded
- * wait that gave up).  The standalone calls (ngram_*, muon_update,
- * gptx_gemm_bf16) share ONE such word per device, not one per stream: a status
+ * wait that gave up, GPT_ERR_NONFINITE for a loss or gradient norm that is not
+ * finite).  The standalone calls (ngram_*, muon_update, grad_clip, linear_ce_*,
+ * the GEMMs) share ONE such word per device, not one per stream: a status
  * read here may report a fault raised by another stream's standalone call on
  * the same device, and clearing it hides that fault from that stream's caller.
  * Callers that run standalone calls on several streams at once should read the
@@ -420,6 +421,85 @@ int fp8_quantize(const void* x, int dtype, long long n, uint8_t* q, float* scale
  */
 int gptx_gemm_fp8(int M, int N, int K, const uint8_t* A, long long lda, const uint8_t* B, long long ldb,
                   const float* scale_a, const float* scale_b, int out_dtype, void* C, long long ldc, void* stream);
+
+/* ---- FP8 (e4m3) with a scale for each group of 128 elements ------------- */
+
+/*
+ * Scales of a [rows, cols] matrix of codes: one exponent byte s (a scale of
+ * 2^(s - 127); 255 stands for NaN) per row and group of 128 columns, stored in
+ * 512-byte atoms of 128 rows x 4 groups as the tensor cores read them: the
+ * byte of row r, group b = column / 128 at
+ *   ((b / 4) * ceil(rows / 128) + r / 128) * 512 + 16 (r % 32)
+ *   + 4 (r % 128 / 32) + b % 4.
+ * What the last atoms hold beyond the matrix must not be 255 (the quantizer
+ * writes 127).  Host only.
+ */
+int fp8_block_scale_bytes(long long rows, long long cols, size_t* bytes);
+
+/*
+ * e4m3 quantization with a power-of-two scale for each group: the least 2^e
+ * with amax <= 448 * 2^e over the group (1 when amax is 0, at least 2^-127),
+ * code = e4m3(x / 2^e) to nearest even.  Dividing by a power of two is exact, so
+ * codes and scales depend on x alone.  square = 0: a group is 128 consecutive
+ * elements of a row (activations and gradients); square != 0: a block of 128 x
+ * 128 (weights), whose 128 rows carry the same byte.  A group that holds an
+ * infinity or a NaN gets the scale NaN and NaN codes, so that every product it
+ * enters is NaN instead of a saturated number.
+ * x: device [rows, cols] of `dtype` (GPT_DTYPE_F32 or GPT_DTYPE_BF16), row pitch
+ * ldx elements (16-byte aligned rows load faster).  q: device uint8 [rows, cols],
+ * row pitch ldq bytes, with `scales`; qt: device uint8 [cols, rows], pitch ldqt, the
+ * codes of the transpose with scales_t, its groups running along x's rows; either
+ * of q and qt may be null, x is read once for both.  Code addresses and pitches
+ * are multiples of 16 bytes; bytes between cols and ldq are left as they are.
+ * The forward product of a linear layer takes x (square = 0) and W (square = 1);
+ * its data gradient dY and the transposed W; its weight gradient the transposed dY
+ * and the transposed x.  Asynchronous on `stream`.
+ */
+int fp8_block_quantize(const void* x, int dtype, long long rows, long long cols, long long ldx, int square, uint8_t* q,
+                       long long ldq, uint8_t* scales, uint8_t* qt, long long ldqt, uint8_t* scales_t, void* stream);
+
+/* Device workspace bytes gptx_gemm_fp8_block() needs (0 when K is not split). */
+int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes);
+
+/*
+ * C[m, n] = (beta ? C[m, n] : 0) + sum_k A[m, k] B[n, k] with A [M, K] and
+ * B [N, K] codes and scales as fp8_block_quantize leaves them, on the tcgen05
+ * tensor cores, which apply the scales (kind::mxf8f6f4.block_scale, fp32
+ * accumulation; SM pairs when gptx_set_gemm_cta_pairs is on).  lda, ldb: row
+ * pitches of the codes in bytes; what lies between K and the pitch is not read.
+ * out_dtype: GPT_DTYPE_F32 or GPT_DTYPE_BF16 (beta only with F32), row pitch ldc
+ * elements.  Addresses and row pitches are multiples of 16 bytes.  A long K with few
+ * output tiles is split, its fp32 partials (in `workspace`, 256-byte aligned) summed in
+ * order: the result is bit-reproducible.  Asynchronous on `stream`; a bounded
+ * wait that gives up is reported by ngram_sync_status().
+ */
+int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long long lda, const uint8_t* scales_a,
+                        const uint8_t* B, long long ldb, const uint8_t* scales_b, int out_dtype, void* C, long long ldc,
+                        int beta, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- gradient clipping over many tensors -------------------------------- */
+
+/* Device workspace bytes grad_clip() needs for n tensors. */
+int grad_clip_workspace_bytes(int n, size_t* bytes);
+
+/*
+ * The global L2 norm of n gradient tensors and the clip of the training step
+ * (torch's clip_grad_norm_) on them:
+ *   norm = sqrt(sum_i sum_j grads[i][j]^2), coef = min(1, max_norm / (norm + 1e-6)),
+ *   outs[i][j] = coef * grads[i][j].
+ * grads, outs, sizes, dtypes: host arrays [n] of device addresses, element
+ * counts (0 allowed) and GPT_DTYPE_F32 / GPT_DTYPE_BF16, read before the call
+ * returns.  outs = null clips in place (and writes nothing when coef is 1);
+ * otherwise outs[i] has grads[i]'s type and size.  An output must not
+ * overlap another output or another tensor's input (refused).  Any element-aligned address (16 bytes
+ * are faster).  max_norm = 0: no scaling.  The squares are summed in fp64
+ * in a fixed order (bit-reproducible); a norm that is not finite leaves the
+ * gradients unscaled and is reported as GPT_ERR_NONFINITE by the next
+ * ngram_sync_status().  norm_out: device float, nullable.  workspace: device, 256-byte
+ * aligned.  Asynchronous on `stream`.
+ */
+int grad_clip(int n, const void* const* grads, void* const* outs, const long long* sizes, const int* dtypes,
+              float max_norm, float* norm_out, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---- Muon (matrix-parameter optimizer) --------------------------------- */
 
