@@ -92,6 +92,10 @@ _SIGS = {
     "fp8_block_quantize": [_P, _I, _LL, _LL, _LL, _I, _P, _LL, _P, _P, _LL, _P, _P],
     "gptx_gemm_fp8_block_workspace_bytes": [_I, _I, _I, ctypes.POINTER(_SZ)],
     "gptx_gemm_fp8_block": [_I, _I, _I, _P, _LL, _P, _P, _LL, _P, _I, _P, _LL, _I, _P, _SZ, _P],
+    "linear_ce_workspace_bytes": [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)],
+    "linear_ce_forward": [_P, _LL, _P, _LL, _I, _I, _I, _I, _P, _F, _P, _P, _P, _I, _P, _SZ, _P],
+    "linear_ce_backward": [_P, _LL, _P, _LL, _I, _I, _I, _I, _P, _F, _P, _P, _P, _P, _LL, _P, _LL, _I, _I, _I, _P,
+                           _SZ, _P],
     "grad_clip_workspace_bytes": [_I, ctypes.POINTER(_SZ)],
     "grad_clip": [_I, _P, _P, _P, _P, _F, _P, _P, _SZ, _P],
     "trigram_tally_workspace_bytes": [_LL, _I, ctypes.POINTER(_SZ)],
@@ -369,6 +373,34 @@ def gptx_gemm_fp8_block(M, N, K, A, lda, scales_a, B, ldb, scales_b, out_dtype, 
     return _check(_lib.gptx_gemm_fp8_block(M, N, K, _ptr(A), lda, _ptr(scales_a), _ptr(B), ldb, _ptr(scales_b),
                                            out_dtype, _ptr(C), ldc, int(beta), _ptr(workspace), ws_bytes,
                                            _stream(stream)), "gptx_gemm_fp8_block")
+
+
+def linear_ce_workspace_bytes(N, V, d, dtype, backward, vocab_piece=0):
+    b = ctypes.c_size_t()
+    _check(_lib.linear_ce_workspace_bytes(N, V, d, dtype, int(backward), vocab_piece, ctypes.byref(b)),
+           "linear_ce_workspace_bytes")
+    return b.value
+
+
+def linear_ce_forward(x, ldx, w, ldw, dtype, N, V, d, targets, softcap, loss, tok_loss, lse, workspace, ws_bytes,
+                      stream=None, vocab_piece=0):
+    """Cross entropy of softcap(x W^T) against int32 targets [N] (-1: ignored)
+    without storing logits: the mean loss, per-token losses and the rows'
+    log-sum-exp (each may be None)."""
+    return _check(_lib.linear_ce_forward(_ptr(x), ldx, _ptr(w), ldw, dtype, N, V, d, _ptr(targets), float(softcap),
+                                         _ptr(loss), _ptr(tok_loss), _ptr(lse), vocab_piece, _ptr(workspace), ws_bytes,
+                                         _stream(stream)), "linear_ce_forward")
+
+
+def linear_ce_backward(x, ldx, w, ldw, dtype, N, V, d, targets, softcap, lse, dloss, dtok, dx, lddx, dw, lddw,
+                       dw_dtype, dw_beta, workspace, ws_bytes, stream=None, vocab_piece=0):
+    """Gradients of linear_ce_forward's mean loss (scaled by the device scalar
+    dloss, None: 1) or of its per-token losses (dtok [N]) with respect to x
+    (dx) and W (dw); either may be None."""
+    return _check(_lib.linear_ce_backward(_ptr(x), ldx, _ptr(w), ldw, dtype, N, V, d, _ptr(targets), float(softcap),
+                                          _ptr(lse), _ptr(dloss), _ptr(dtok), _ptr(dx), lddx, _ptr(dw), lddw, dw_dtype,
+                                          int(dw_beta), vocab_piece, _ptr(workspace), ws_bytes, _stream(stream)),
+                  "linear_ce_backward")
 
 
 def grad_clip_workspace_bytes(n):

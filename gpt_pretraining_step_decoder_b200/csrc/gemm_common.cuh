@@ -28,6 +28,10 @@ enum EpiMode {
   EPI_QKV = 6,        // fused q|k|v projection output (tensor-core path, 128-wide heads):
                       // q, k heads rotated (RoPE) and RMS-normalised per head, v heads plus
                       // the value-table row; C(act) = result
+  EPI_LSE = 8,        // no output: per (column half tile, row) m = max z and s = sum exp(z - m),
+                      // z = softcap(acc), into stats; z at the row's target column into ztgt
+  EPI_DLOGITS = 9,    // C(bf16) = (exp(z - lse) - [column = target]) * row_scale, times the
+                      // softcap's slope 1 - (z / softcap)^2 (tensor-core path only, as the former)
   EPI_AXPBY = 7,      // C(act) = alpha * acc + aux_scale * aux(act), aux of C's shape and ld
                       // (the Newton-Schulz polynomial's combinations; tensor-core path)
 };
@@ -41,7 +45,7 @@ struct GemmEpilogue {
   float alpha;
   int beta;
   float softcap;    // EPI_LOGITS: 0 = off, else z = softcap * tanh(acc / softcap)
-  float2* stats;    // EPI_LOGITS: [M, n_tiles] (max, sum of exp(z - max))
+  float2* stats;    // EPI_LOGITS: [M, n_tiles] (max, sum of exp(z - max)); EPI_LSE: [n_tiles, M]
   const int32_t* targets;  // EPI_LOGITS: target column per row (< 0: none), nullable
   float* ztgt;             // EPI_LOGITS: z at the target column per row
   // EPI_QKV: RoPE turns per position of the 64 frequencies ([64] float2, an
@@ -58,6 +62,11 @@ struct GemmEpilogue {
   const float* scale_a;
   const float* scale_b;
   float aux_scale;  // EPI_AXPBY
+  // EPI_DLOGITS: log-sum-exp and gradient scale per row; columns are those of
+  // a piece of the vocabulary that starts at col0 (targets count from 0)
+  const float* lse;
+  const float* row_scale;
+  int col0;
 };
 
 template <typename act_t>

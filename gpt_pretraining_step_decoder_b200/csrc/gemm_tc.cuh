@@ -82,6 +82,8 @@ enum KMode {
   K_DRELU2,       // bf16 2 sqrt(aux) acc
   K_LOGITS,       // bf16 exp(z - tile max), z = softcap(acc), + per-tile row statistics
   K_QKV,          // bf16 q|k|v with RoPE + QK-norm (+ value-table row) per 128-wide head
+  K_LSE,          // no output: row statistics of z = softcap(acc) per half tile, target logit
+  K_DLOGITS,      // bf16 gradient of the cross entropy with respect to the logits
   K_AXPBY,        // bf16 acc + aux_scale * aux (aux streamed like the ReLU^2 backward's)
 };
 
@@ -833,8 +835,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (!warp_wait(&tfull[acc], acc_phase, abort_flag, p.err)) { ok = false; break; }
       tc_fence_after();
       float rmax = -INFINITY, rsum = 0.f;
+      float row_lse = 0.f, row_g = 0.f;
       const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN + ccol;
       int ytgt = -1;
+      if constexpr (KM == K_DLOGITS) {
+        if (m < p.M) {
+          ytgt = e.targets[m] - e.col0;
+          row_lse = e.lse[m];
+          row_g = e.row_scale[m];
+        }
+      }
+      if constexpr (KM == K_LSE) ytgt = m < p.M ? e.targets[m] : -1;
       // The store, ReLU^2 and fp32 epilogues take the warp's whole half tile
       // from TMEM into registers at once and hand the accumulator back to the
       // MMA warp before any arithmetic or store, so the MMA of the tile after
@@ -859,6 +870,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if constexpr (CG == 2) mbar_arrive_cluster(tempty0 + acc * 8);
           else mbar_arrive(&tempty[acc]);
         }
+      }
+      if constexpr (KM == K_LSE) {
+        // the half tile's row maximum and sum of exp(z - max), all from
+        // registers: nothing but these two numbers leaves the tile
+        if (e.softcap > 0.f) softcap_block<HALF>(accr, e.softcap);
+        const int nv = p.N - n0;  // columns of the half tile that exist
+        if (nv < HALF) {
+#pragma unroll
+          for (int i = 0; i < HALF; ++i) accr[i] = i < nv ? accr[i] : -INFINITY;
+        }
+        const int yo = ytgt - n0;
+        if (ytgt >= 0 && yo >= 0 && yo < HALF && yo < nv) {  // rare: this row's target logit
+          float zt = 0.f;
+#pragma unroll
+          for (int i = 0; i < HALF; ++i) zt = (i == yo) ? accr[i] : zt;
+          e.ztgt[m] = zt;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < HALF; ++i) mx[i & 3] = fmaxf(mx[i & 3], accr[i]);
+        rmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // a row of -inf only sums to 0 instead of exp(-inf + inf)
+        constexpr float L2E = 1.4426950408889634f;
+        const float nb = rmax == -INFINITY ? 0.f : -rmax * L2E;
+        float ps[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < HALF; i += 2) {
+          float x0, x1, p0, p1;
+          fma2(x0, x1, accr[i], accr[i + 1], L2E, nb);
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(x0));
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(x1));
+          add2(ps[(i >> 1) & 7], ps[((i >> 1) + 4) & 7], p0, p1);
+        }
+        rsum = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+        if (nv > 0 && m < p.M) e.stats[(long long)(nt * 2 + (ew >> 2)) * p.M + m] = make_float2(rmax, rsum);
       }
       if constexpr (KM == K_LOGITS) {
         // first pass over the accumulator: the half tile's row maximum, so
@@ -1006,6 +1052,37 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
           rsum += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+        } else if constexpr (KM == K_DLOGITS) {
+          // (exp(z - lse) - [target]) * scale; the exponent's argument stays a
+          // difference of fp32 numbers, two at a time
+          constexpr float L2E = 1.4426950408889634f;
+          const float nb = -row_lse * L2E;
+          const int yo = ytgt - nc;
+          if (e.softcap > 0.f) {
+            softcap_block<64>(v, e.softcap);
+            const float rc = 1.f / e.softcap;
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              const float t = v[i] * rc;
+              float pr;
+              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(pr) : "f"(fmaf(v[i], L2E, nb)));
+              v[i] = row_g != 0.f ? (pr - (i == yo ? 1.f : 0.f)) * fmaf(-t, t, 1.f) * row_g : 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              float x0, x1, p0, p1;
+              fma2(x0, x1, v[i], v[i + 1], L2E, nb);
+              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(x0));
+              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(x1));
+              v[i] = row_g != 0.f ? p0 * row_g : 0.f;  // a row without a gradient stays out, whatever its logits
+              v[i + 1] = row_g != 0.f ? p1 * row_g : 0.f;
+            }
+            if (yo >= 0 && yo < 64) {  // rare: the target is in this block
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i] -= (i == yo) ? row_g : 0.f;
+            }
+          }
         } else if constexpr (KM == K_RELU2) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) { const float r = fmaxf(v[i], 0.f); v[i] = r * r; }
@@ -1079,7 +1156,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         return true;
       };
-      if constexpr (PRE) {
+      if constexpr (PRE && KM != K_LSE) {
 #pragma unroll
         for (int c = 0; c < HALF / CW; ++c) {
           if (c >= nblk) break;  // warp-uniform
@@ -1088,7 +1165,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int i = 0; i < CW; ++i) v[i] = accr[c * CW + i];
           if (!out_block(c, v)) { ok = false; break; }
         }
-      } else if constexpr (KM != K_QKV) {
+      } else if constexpr (KM != K_QKV && KM != K_LSE) {
 #pragma unroll 1
         for (int c = 0; c < nblk; ++c) {
           float v[64];

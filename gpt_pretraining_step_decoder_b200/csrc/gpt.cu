@@ -326,6 +326,8 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
     const uint64_t dims[2] = {(uint64_t)N, (uint64_t)M}, str[1] = {(uint64_t)e.ldc * 4};
     const uint32_t box[2] = {32, 32};
     TRY(make_tmap_gen(&tcm, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, e.C, dims, str, box));
+  } else if (e.mode == EPI_LSE) {
+    tcm = ta;  // no output
   } else {
     TRY(make_tmap(&tcm, e.C, N, M, e.ldc, 64, 32));
   }
@@ -345,6 +347,8 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
   else if (e.mode == EPI_DRELU2) km = tc::K_DRELU2;
   else if (e.mode == EPI_QKV) km = tc::K_QKV;
   else if (e.mode == EPI_AXPBY) km = tc::K_AXPBY;
+  else if (e.mode == EPI_LSE) km = tc::K_LSE;
+  else if (e.mode == EPI_DLOGITS) km = tc::K_DLOGITS;
   else km = tc::K_LOGITS;
   if (km == tc::K_QKV && BN != 256) return fail(GPT_ERR_ARG, "QKV epilogue needs 256-column tiles (N >= 256)");
   if (b3) {
@@ -371,6 +375,8 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
     case tc::K_DRELU2: TRY((gemm_tc_launch_k<BN, tc::K_DRELU2, CG>(ta, tb, tcm, taux, p, st))); break;
     case tc::K_QKV: TRY((gemm_tc_launch_k<BN, tc::K_QKV, CG>(ta, tb, tcm, taux, p, st))); break;
     case tc::K_AXPBY: TRY((gemm_tc_launch_k<BN, tc::K_AXPBY, CG>(ta, tb, tcm, taux, p, st))); break;
+    case tc::K_LSE: TRY((gemm_tc_launch_k<BN, tc::K_LSE, CG>(ta, tb, tcm, taux, p, st))); break;
+    case tc::K_DLOGITS: TRY((gemm_tc_launch_k<BN, tc::K_DLOGITS, CG>(ta, tb, tcm, taux, p, st))); break;
     default: TRY((gemm_tc_launch_k<BN, tc::K_LOGITS, CG>(ta, tb, tcm, taux, p, st))); break;
   }
   }
@@ -511,7 +517,7 @@ static int gemm(const GemmCtx& g, int M, int N, int K, GemmOperand A, GemmOperan
     return GPT_OK;
   }
   const bool f32out = e.mode == EPI_ACCUM_F32 || e.mode == EPI_STORE_F32;
-  const bool split_ok = allow_split && f32out;
+  const bool split_ok = allow_split && (f32out || e.mode == EPI_STORE);
   auto splits_for = [&](int bn, int cg = 1) {
     if (!split_ok) return 1;
     int s = pick_splits(M, N, K, bn, cg);
@@ -548,6 +554,8 @@ static GemmEpilogue epi(int mode, void* C, long long ldc, int beta = 0, void* C2
   e.rope = nullptr; e.rstd_q = e.rstd_k = nullptr; e.hv = nullptr; e.rv = nullptr;
   e.scale_a = e.scale_b = nullptr;
   e.aux_scale = 0.f;
+  e.lse = e.row_scale = nullptr;
+  e.col0 = 0;
   e.T = e.H = e.qk_norm = 0; e.eps = 0.f;
   return e;
 }

@@ -1,11 +1,13 @@
 // train_ops.cuh -- C entry points of the standalone training operators on the
-// caller's tensors: block-scaled FP8 quantization and product, and gradient
-// clipping over many tensors.  Included once, by gpt.cu, whose helpers
+// caller's tensors: block-scaled FP8 quantization and product, cross entropy
+// over a large vocabulary with its gradient, and gradient clipping over many
+// tensors.  Included once, by gpt.cu, whose helpers
 // (status codes, tensor maps, launches, GEMM dispatch) it uses.  Documented in
 // include/gpt.h.
 #pragma once
 #include "clip.cuh"
 #include "fp8_block.cuh"
+#include "linear_ce.cuh"
 
 // ======================================================================== device of a call
 // A call runs on the device of its tensors, made current for the call and
@@ -197,6 +199,203 @@ extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long l
   if (pl.bn == 192) return gemm_f8b_launch<192, 2>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
   if (pl.cg == 2) return gemm_f8b_launch<128, 2>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
   return gemm_f8b_launch<128, 1>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
+}
+
+// ======================================================================== cross entropy without stored logits
+// Columns of the vocabulary that the backward pass (and the fp32 forward pass)
+// takes at a time.  bf16: as many 256-column tiles as keep the piece's dz
+// [N, width] within 512 MB, but no fewer than half of that, chosen so that the
+// tiles of the weight gradient (width x d) and of the logits (N x width) fill
+// whole waves of SM pairs over all pieces.  More pieces cost a pass over the
+// fp32 dx each, fewer cost memory.
+static int ce_piece(int N, int V, int d, int dtype, int asked) {
+  const int tiles = cdiv(V, 256);
+  if (asked > 0) return std::min(V, 64 * cdiv(asked, 64));
+  const long long budget = 512LL << 20, col_bytes = std::max(N, 1) * (long long)(dtype == GPT_DTYPE_BF16 ? 2 : 4) * 256;
+  const int most = (int)std::max<long long>(1, std::min<long long>(tiles, budget / col_bytes));
+  if (most >= tiles || dtype != GPT_DTYPE_BF16) return std::min(V, most * 256);
+  const int units = std::max(1, device_sms() / 2);
+  auto waves = [&](long long t) { return (double)((t + units - 1) / units); };
+  int best = most;
+  double best_cost = 1e300;
+  for (int w = most; w >= (most + 1) / 2; --w) {
+    double cost = 0.0;
+    for (int v = 0; v < tiles; v += w) {
+      const int n = std::min(w, tiles - v);
+      cost += waves((long long)n * cdiv(N, 256)) * d + waves((long long)n * cdiv(d, 256)) * N;
+    }
+    cost += cdiv(tiles, w) * (waves((long long)cdiv(N, 256) * cdiv(d, 256)) * 0.04 * 256 * w);  // dx read and written
+    if (cost < best_cost) { best_cost = cost; best = w; }
+  }
+  return std::min(V, best * 256);
+}
+
+// Byte offsets of the operator's scratch inside the caller's workspace.
+struct CeWs {
+  size_t stats, ztgt, part, rowg, dz, dx, splitk, total;
+  int piece, n_tiles;
+  long long splitk_elems;
+};
+static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) {
+  CeWs w = {};
+  Carver cv;
+  const bool lp = dtype == GPT_DTYPE_BF16;
+  w.piece = ce_piece(N, V, d, dtype, asked);
+  if (!backward) {
+    w.n_tiles = lp ? cdiv(V, V >= 256 ? 128 : 64) : 1;
+    w.stats = cv.take((size_t)w.n_tiles * N * 8);
+    w.ztgt = cv.take((size_t)N * 4);
+    w.part = cv.take((size_t)cdiv(N, 32) * 16);
+    if (!lp) w.dz = cv.take((size_t)N * w.piece * 4);
+  } else {
+    w.rowg = cv.take((size_t)N * 4);
+    w.dz = cv.take((size_t)N * (lp ? 64 * cdiv(w.piece, 64) : w.piece) * (lp ? 2 : 4));
+    if (lp) {
+      w.dx = cv.take((size_t)N * d * 4);
+      // split-K partials, for products of few output tiles
+      w.splitk_elems = std::min<long long>(16LL * std::max<long long>(N, w.piece) * d, 32LL << 20);
+      w.splitk = cv.take((size_t)w.splitk_elems * 4);
+    }
+  }
+  w.total = cv.take(0);
+  return w;
+}
+
+static int ce_check(const char* fn, const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V,
+                    int d, const int32_t* targets, float softcap) {
+  if (N < 0 || V < 1 || d < 1 || !w || (N > 0 && (!x || !targets)) || ldx < d || ldw < d || !(softcap >= 0.f) ||
+      std::isinf(softcap))
+    return fail(GPT_ERR_ARG, "%s: bad argument", fn);
+  if (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16) return fail(GPT_ERR_ARG, "%s: bad dtype", fn);
+  if (dtype == GPT_DTYPE_BF16 && (d % 8 || ldx % 8 || ldw % 8 || misaligned(x, 16) || misaligned(w, 16)))
+    return fail(GPT_ERR_ARG, "%s: bf16 rows must be 16-byte aligned: d, ldx and ldw multiples of 8", fn);
+  if (dtype == GPT_DTYPE_F32 && (misaligned(x, 4) || misaligned(w, 4)))
+    return fail(GPT_ERR_ARG, "%s: x or w is not aligned to its elements", fn);
+  if (misaligned(targets, 4)) return fail(GPT_ERR_ARG, "%s: targets are not aligned to their elements", fn);
+  return GPT_OK;
+}
+
+extern "C" int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int vocab_piece, size_t* bytes) {
+  if (!bytes || N < 0 || V < 1 || d < 1 || vocab_piece < 0 || (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16))
+    return fail(GPT_ERR_ARG, "linear_ce_workspace_bytes: bad argument");
+  *bytes = ce_ws_plan(N, V, d, dtype, backward != 0, vocab_piece).total;
+  return GPT_OK;
+}
+
+extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V,
+                                 int d, const int32_t* targets, float softcap, float* loss, float* tok_loss, float* lse,
+                                 int vocab_piece, void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "linear_ce_forward";
+  TRY(ce_check(fn, x, ldx, w, ldw, dtype, N, V, d, targets, softcap));
+  if (!loss && !tok_loss && !lse) return fail(GPT_ERR_ARG, "%s: no output", fn);
+  if (vocab_piece < 0) return fail(GPT_ERR_ARG, "%s: bad argument", fn);
+  const CeWs p = ce_ws_plan(N, V, d, dtype, 0, vocab_piece);
+  if (!workspace || ws_bytes < p.total) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, p.total);
+  if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
+  cudaStream_t st = (cudaStream_t)stream;
+  ON_DEVICE_OF(fn, workspace);
+  CHECK_PTR(fn, x); CHECK_PTR(fn, w); CHECK_PTR(fn, targets); CHECK_PTR(fn, loss); CHECK_PTR(fn, tok_loss); CHECK_PTR(fn, lse);
+  if (N == 0) {
+    if (loss) CUDA_TRY(cudaMemsetAsync(loss, 0, 4, st));
+    return GPT_OK;
+  }
+  unsigned* err = nullptr;
+  CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
+  uint8_t* b = static_cast<uint8_t*>(workspace);
+  float2* stats = reinterpret_cast<float2*>(b + p.stats);
+  float* ztgt = reinterpret_cast<float*>(b + p.ztgt);
+  double2* part = reinterpret_cast<double2*>(b + p.part);
+  const GemmCtx g{dtype == GPT_DTYPE_BF16, nullptr, 0, err, st, nullptr};
+  if (g.bf16) {
+    GemmEpilogue e = epi(EPI_LSE, nullptr, V);
+    e.softcap = softcap; e.stats = stats; e.targets = targets; e.ztgt = ztgt;
+    TRY(gemm(g, N, V, d, op_k(x, ldx), op_k(w, ldw), e));
+  } else {
+    float* z = reinterpret_cast<float*>(b + p.dz);
+    for (int v0 = 0; v0 < V; v0 += p.piece) {
+      const int width = std::min(p.piece, V - v0);
+      TRY(gemm(g, N, width, d, op_k(x, ldx), op_k(static_cast<const float*>(w) + v0 * ldw, ldw),
+               epi(EPI_STORE_F32, z, width)));
+      ++g_launches; launch_pdl(ce_piece_stats_kernel, N, 256, 0, st, (const float*)z, width, v0, v0 == 0 ? 1 : 0, softcap,
+                               targets, N, stats, ztgt);
+      LAUNCH_CHECK();
+    }
+  }
+  const int blocks = cdiv(N, 32);
+  ++g_launches; launch_pdl(ce_combine_kernel, blocks, 1024, 0, st, (const float2*)stats, p.n_tiles, N, V, targets,
+                           (const float*)ztgt, lse, tok_loss, part, err);
+  LAUNCH_CHECK();
+  ++g_launches; launch_pdl(ce_mean_kernel, 1, 1024, 0, st, (const double2*)part, blocks, loss, err);
+  LAUNCH_CHECK();
+  return GPT_OK;
+}
+
+extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V,
+                                  int d, const int32_t* targets, float softcap, const float* lse, const float* dloss,
+                                  const float* dtok, void* dx, long long lddx, void* dw, long long lddw, int dw_dtype,
+                                  int dw_beta, int vocab_piece, void* workspace, size_t ws_bytes, void* stream) {
+  const char* fn = "linear_ce_backward";
+  TRY(ce_check(fn, x, ldx, w, ldw, dtype, N, V, d, targets, softcap));
+  const bool lp = dtype == GPT_DTYPE_BF16;
+  if ((N > 0 && !lse) || (!dx && !dw) || (dx && lddx < d) || (dw && lddw < d) || (dloss && dtok) || vocab_piece < 0)
+    return fail(GPT_ERR_ARG, "%s: bad argument", fn);
+  if (dw && ((dw_dtype != GPT_DTYPE_F32 && dw_dtype != GPT_DTYPE_BF16) || (!lp && dw_dtype != GPT_DTYPE_F32) ||
+             (dw_beta && dw_dtype != GPT_DTYPE_F32)))
+    return fail(GPT_ERR_ARG, "%s: bad dw_dtype (bf16 only with bf16 inputs, accumulation only in fp32)", fn);
+  if (lp && ((dx && (misaligned(dx, 16) || lddx % 8)) ||
+             (dw && (misaligned(dw, 16) || (lddw * (long long)dtype_size(dw_dtype)) % 16))))
+    return fail(GPT_ERR_ARG, "%s: gradient rows must be 16-byte aligned", fn);
+  if (!lp && (misaligned(dx, 4) || misaligned(dw, 4))) return fail(GPT_ERR_ARG, "%s: a gradient is not aligned to its elements", fn);
+  const CeWs p = ce_ws_plan(N, V, d, dtype, 1, vocab_piece);
+  if (!workspace || ws_bytes < p.total) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, p.total);
+  if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
+  cudaStream_t st = (cudaStream_t)stream;
+  ON_DEVICE_OF(fn, workspace);
+  CHECK_PTR(fn, x); CHECK_PTR(fn, w); CHECK_PTR(fn, targets); CHECK_PTR(fn, lse); CHECK_PTR(fn, dloss); CHECK_PTR(fn, dtok);
+  CHECK_PTR(fn, dx); CHECK_PTR(fn, dw);
+  if (N == 0) {  // no rows: nothing but a weight gradient of zero
+    if (dw && !dw_beta)
+      CUDA_TRY(cudaMemset2DAsync(dw, lddw * dtype_size(dw_dtype), 0, (size_t)d * dtype_size(dw_dtype), V, st));
+    return GPT_OK;
+  }
+  unsigned* err = nullptr;
+  CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
+  uint8_t* b = static_cast<uint8_t*>(workspace);
+  float* rowg = reinterpret_cast<float*>(b + p.rowg);
+  ++g_launches; launch_pdl(ce_row_scale_kernel, std::min(32, cdiv(N, 1024)), 1024, 0, st, targets, N, V, dloss, dtok, rowg, err);
+  LAUNCH_CHECK();
+  const GemmCtx g{lp, reinterpret_cast<float*>(b + p.splitk), p.splitk_elems, err, st, nullptr};
+  const size_t es = dtype_size(dtype);
+  void* dz = b + p.dz;
+  float* acc = lp ? reinterpret_cast<float*>(b + p.dx) : static_cast<float*>(dx);
+  const long long ldacc = lp ? d : lddx;
+  for (int v0 = 0; v0 < V; v0 += p.piece) {
+    const int width = std::min(p.piece, V - v0);
+    const uint8_t* wp = static_cast<const uint8_t*>(w) + (size_t)v0 * ldw * es;
+    long long ldz = width;
+    if (lp) {
+      ldz = 64 * cdiv(width, 64);
+      GemmEpilogue e = epi(EPI_DLOGITS, dz, ldz);
+      e.softcap = softcap; e.targets = targets; e.col0 = v0; e.lse = lse; e.row_scale = rowg;
+      TRY(gemm(g, N, width, d, op_k(x, ldx), op_k(wp, ldw), e));
+    } else {
+      TRY(gemm(g, N, width, d, op_k(x, ldx), op_k(wp, ldw), epi(EPI_STORE_F32, dz, width)));
+      ++g_launches; launch_pdl(ce_piece_grad_kernel, N, 256, 0, st, (float*)dz, width, v0, softcap, targets, lse, (const float*)rowg);
+      LAUNCH_CHECK();
+    }
+    if (dx) TRY(gemm(g, N, d, width, op_k(dz, ldz), op_mn(wp, ldw), epi(EPI_ACCUM_F32, acc, ldacc, v0 > 0), true));
+    if (dw) {
+      uint8_t* out = static_cast<uint8_t*>(dw) + (size_t)v0 * lddw * dtype_size(dw_dtype);
+      const GemmEpilogue e = dw_dtype == GPT_DTYPE_BF16 ? epi(EPI_STORE, out, lddw) : epi(EPI_ACCUM_F32, out, lddw, dw_beta);
+      TRY(gemm(g, width, d, N, op_mn(dz, ldz), op_mn(x, ldx), e, true));
+    }
+  }
+  if (dx && lp) {
+    const int blocks = (int)std::min<long long>(((long long)N * d / 4 + 255) / 256, 8LL * device_sms());
+    ++g_launches; launch_pdl(ce_dx_kernel, blocks, 256, 0, st, (const float*)acc, N, d, (bf16*)dx, lddx);
+    LAUNCH_CHECK();
+  }
+  return GPT_OK;
 }
 
 // ======================================================================== gradient clipping

@@ -477,6 +477,57 @@ int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long long lda, co
                         const uint8_t* B, long long ldb, const uint8_t* scales_b, int out_dtype, void* C, long long ldc,
                         int beta, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---- cross entropy over a large vocabulary without stored logits --------- */
+
+/*
+ * Device workspace bytes of linear_ce_forward() (backward = 0) and
+ * linear_ce_backward() (backward != 0).  vocab_piece: columns of the vocabulary
+ * taken at a time (0 = chosen, about 512 MB for N rows of them; the bf16
+ * forward pass keeps no logits at all and takes none).  Pass the same value to
+ * the call.
+ */
+int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int vocab_piece, size_t* bytes);
+
+/*
+ * Loss of the LM head on the caller's hidden states ("$1000 tier nanochat run",
+ * `GPT.forward`: softcapped logits in fp32, F.cross_entropy(ignore_index=-1)):
+ *   z = softcap * tanh(x W^T / softcap) (softcap = 0: z = x W^T),
+ *   lse[i] = log sum_v exp(z[i, v]), tok_loss[i] = lse[i] - z[i, targets[i]],
+ *   *loss = mean of tok_loss over the targets that are not ignored (0 if none).
+ * x: device [N, d], row pitch ldx; w: device [V, d], row pitch ldw (elements),
+ * both of `dtype`; bf16 rows are 16-byte aligned (d, ldx, ldw multiples of 8).
+ * targets: device int32 [N], -1 = ignored (tok_loss 0); others outside [0, V) are
+ * ignored and set GPT_ERR_INPUT on the standalone error word, a mean that is not
+ * finite GPT_ERR_NONFINITE (ngram_sync_status).  loss, tok_loss [N], lse [N]: device
+ * float, each nullable; keep lse for the backward pass.  The logits are formed
+ * in tiles on the tensor cores with fp32 accumulation and reduced there (fp32 mode:
+ * FFMA, a piece of fp32 logits at a time in the workspace); sums are formed
+ * in a fixed order.  N = 0 gives a loss of 0.  workspace: 256-byte aligned.
+ * Asynchronous on `stream`.
+ */
+int linear_ce_forward(const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V, int d,
+                      const int32_t* targets, float softcap, float* loss, float* tok_loss, float* lse, int vocab_piece,
+                      void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of that loss, the logits formed once more piece by piece:
+ *   dz[i, v] = (exp(z - lse[i]) - [v == targets[i]]) * g[i] * (1 - (z / softcap)^2),
+ *   dx = dz W, dW = dz^T x,
+ * with g[i] = *dloss / (number of targets that are not ignored) (dloss null: 1),
+ * or g[i] = dtok[i] when dtok (device float [N], the gradient of tok_loss) is given;
+ * not both.  Ignored rows get dx = 0; their x must be finite (it enters dW times
+ * zero).  dx: [N, d] of `dtype`, row pitch lddx; dw: [V, d] of dw_dtype (bf16
+ * inputs: BF16 or F32; fp32 inputs: F32), row pitch lddw, overwritten or, with
+ * dw_beta != 0 (F32 only), added to; either gradient may be null.  dz of a piece is
+ * rounded to bf16 for the tensor cores (as the training step does) and dx
+ * is summed over the pieces in fp32 and rounded once.  Bit-reproducible.
+ * Asynchronous on `stream`.
+ */
+int linear_ce_backward(const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V, int d,
+                       const int32_t* targets, float softcap, const float* lse, const float* dloss, const float* dtok,
+                       void* dx, long long lddx, void* dw, long long lddw, int dw_dtype, int dw_beta, int vocab_piece,
+                       void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- gradient clipping over many tensors -------------------------------- */
 
 /* Device workspace bytes grad_clip() needs for n tensors. */

@@ -92,3 +92,53 @@ def test_clip_workspace_refusal():
     assert g.grad_clip_workspace_bytes(1025) == 2 * need
     with pytest.raises(g.GptError):
         g.grad_clip_workspace_bytes(-1)
+
+
+CE = dict(x=A, ldx=64, w=B, ldw=64, dtype=g.DTYPE_BF16, N=10, V=100, d=64, t=C, cap=0.0)
+
+
+def ce_forward(loss=D, ws=WS, ws_bytes=1 << 30, piece=0, **kw):
+    a = dict(CE, **kw)
+    return g._lib.linear_ce_forward(*a.values(), loss, None, None, piece, ws, ws_bytes, None)
+
+
+def ce_backward(lse=D, dloss=None, dtok=None, dx=E, lddx=64, dw=E + (1 << 20), lddw=64, dwt=g.DTYPE_BF16, beta=0,
+                ws=WS, ws_bytes=1 << 30, piece=0, **kw):
+    a = dict(CE, **kw)
+    return g._lib.linear_ce_backward(*a.values(), lse, dloss, dtok, dx, lddx, dw, lddw, dwt, beta, piece, ws, ws_bytes,
+                                     None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(x=None), dict(w=None), dict(t=None), dict(dtype=2), dict(N=-1), dict(V=0), dict(d=0), dict(ldx=56), dict(ldw=56),
+    dict(cap=-1.0), dict(cap=float("nan")), dict(cap=float("inf")), dict(d=60), dict(ldx=68), dict(ldw=68), dict(x=A + 8),
+    dict(w=B + 2), dict(t=C + 2), dict(dtype=g.DTYPE_F32, x=A + 2), dict(piece=-1), dict(ws=WS + 16),
+])
+def test_ce_refusals(bad):
+    assert ce_forward(**bad) == g.GPT_ERR_ARG
+    assert ce_backward(**bad) == g.GPT_ERR_ARG
+    assert g.gpt_last_error()
+
+
+@pytest.mark.parametrize("bad", [
+    dict(lse=None), dict(dx=None, dw=None), dict(lddx=56), dict(lddw=56), dict(dloss=A, dtok=A), dict(dwt=2),
+    dict(beta=1), dict(dx=E + 8), dict(lddx=68), dict(dw=E + 8), dict(lddw=68), dict(dtype=g.DTYPE_F32),
+])
+def test_ce_backward_refusals(bad):
+    assert ce_backward(**bad) == g.GPT_ERR_ARG
+
+
+def test_ce_workspace():
+    assert ce_forward(loss=None) == g.GPT_ERR_ARG
+    assert g.linear_ce_workspace_bytes(0, 100, 64, g.DTYPE_BF16, 1) >= 0
+    for call, back in ((ce_forward, 0), (ce_backward, 1)):
+        need = g.linear_ce_workspace_bytes(10, 100, 64, g.DTYPE_BF16, back)
+        assert need > 0 and call(ws_bytes=need - 1) == g.GPT_ERR_WORKSPACE
+        assert call(ws=None) == g.GPT_ERR_WORKSPACE
+    # a smaller piece of the vocabulary takes less memory, and the pieces are bounded
+    big = g.linear_ce_workspace_bytes(16384, 65536, 2048, g.DTYPE_BF16, 1)
+    assert g.linear_ce_workspace_bytes(16384, 65536, 2048, g.DTYPE_BF16, 1, 1024) < big < 1 << 30
+    with pytest.raises(g.GptError):
+        g.linear_ce_workspace_bytes(1, 1, 1, 7, 0)
+    with pytest.raises(g.GptError):
+        g.linear_ce_workspace_bytes(1, 1, 1, 0, 0, -1)
