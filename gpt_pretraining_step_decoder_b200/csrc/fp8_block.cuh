@@ -14,14 +14,16 @@
 // tcgen05.cp spreads an atom over tensor memory: lane r % 32, column
 // r % 128 / 32, byte b % 4.
 //
-// One block per 128 x 128 tile, 256 threads; each thread holds 8 rows x 8
-// columns of it in registers, from which both orientations are coded: x is read
-// once.  The transposed codes pass through shared memory (8-byte slots, XORed
-// so that neither the column-wise writes nor the row-wise reads conflict).
-// Memory bounds it: 2 or 4 bytes read and 1 or 2 written per element.
+// Persistent blocks of 512 threads take a 128 x 128 tile at a time; each thread
+// holds 4 rows x 8 columns of it in registers, from which both orientations are
+// coded: x is read once.  A tile arrives by TMA (zeros beyond the matrix) while
+// the one before it is coded; rows that are not 16-byte aligned take plain loads.
+// The transposed codes pass through shared memory (4-byte slots, XORed so that
+// neither the column-wise writes nor the row-wise reads conflict).  Memory bounds
+// it: 2 or 4 bytes read and 1 or 2 written per element.
 #pragma once
 #include <cuda_fp8.h>
-#include "common.cuh"
+#include "gemm_tc.cuh"
 
 // exponent byte of a group from the bits of its largest magnitude: 448 = 1.75 *
 // 2^8, so amax = m 2^k needs 2^(k-8), one more where m > 1.75 (the carry).  0
@@ -48,105 +50,154 @@ struct QuantArgs {
   long long rows, cols, ldx;
   uint8_t* q; long long ldq; uint8_t* sc;     // codes and scales of x; q null: not written
   uint8_t* qt; long long ldqt; uint8_t* sct;  // those of its transpose; qt null: not written
-  int square, vec;                            // vec: 16-byte loads are aligned
+  int square;
+  int tiles;
+  unsigned* err;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(256) fp8_block_quantize_kernel(const T* __restrict__ x, const QuantArgs a) {
-  pdl_wait();
-  __shared__ uint32_t colmax[8][128];
-  __shared__ uint32_t blockmax[8];
-  __shared__ __align__(16) uint2 tr[128 * 16];  // transposed codes: [column][8-row slot]
-  const int cblocks = (int)((a.cols + 127) >> 7);
-  const long long rb = blockIdx.x / cblocks;
-  const int cb = (int)(blockIdx.x % cblocks);
+// |a|, |b| joined to m; a NaN stays
+__device__ __forceinline__ float absmax3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  load4(p, *reinterpret_cast<float(*)[4]>(&v[0]));
+  load4(p + 4, *reinterpret_cast<float(*)[4]>(&v[4]));
+}
+__device__ __forceinline__ void load8(const bf16* p, float (&v)[8]) {
+  const uint4 t = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+}
+
+// (y0, y1) = (x0, x1) * (c0, c1), one instruction
+__device__ __forceinline__ void mul2(float& y0, float& y1, float x0, float x1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(y0), "=f"(y1)
+      : "f"(x0), "f"(x1), "f"(c0), "f"(c1));
+}
+
+constexpr int QUANT_THREADS = 512;
+
+struct QuantShared {
+  float colmax[16][128];    // per warp
+  float rowmax[128];
+  float colinv[128], rowinv[128];
+  uint32_t tr[128 * 32];    // transposed codes: [column][4-row slot]
+  uint64_t full;            // the tile in flight has landed
+  int abort;
+};
+
+// FULL: no bounds to check; TMA: x's tile lies in `buf`, and `next` starts the
+// copy of the tile after it once every thread has read its part.
+template <bool FULL, bool TMA, typename T, typename Next>
+__device__ __forceinline__ void quantize_tile(const T* __restrict__ x, const QuantArgs& a, long long rb, int cb,
+                                              int cblocks, QuantShared& sh, const T* buf, Next next) {
   const long long row0 = rb * 128, col0 = (long long)cb * 128;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = lane >> 4, l = lane & 15;
-  const int r0 = warp * 16 + half * 8;  // this thread's 8 rows and 8 columns of the tile
+  const int slot = warp * 2 + half, r0 = slot * 4;  // this thread's 4 rows and 8 columns of the tile
   const int c0 = l * 8;
-  const bool full = row0 + 128 <= a.rows && col0 + 128 <= a.cols && a.vec;
 
-  float v[8][8];
-  if (full) {
+  float v[4][8];
+  if (TMA) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const T* p = x + (row0 + r0 + i) * a.ldx + col0 + c0;
-      load4(p, *reinterpret_cast<float(*)[4]>(&v[i][0]));
-      load4(p + 4, *reinterpret_cast<float(*)[4]>(&v[i][4]));
-    }
+    for (int i = 0; i < 4; ++i) load8(buf + (r0 + i) * 128 + c0, v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const long long r = row0 + r0 + i, c = col0 + c0 + j;
         v[i][j] = r < a.rows && c < a.cols ? to_f(x[r * a.ldx + c]) : 0.f;
       }
   }
-  // largest magnitudes, as bit patterns (they order like the values; infinities
-  // and NaN come out on top)
-  uint32_t rmax[8], cmax[8];
+  // largest magnitudes (an infinity comes out on top, a NaN as NaN)
+  float rmax[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) { rmax[i] = 0u; cmax[i] = 0u; }
+  for (int i = 0; i < 4; ++i) {
+    rmax[i] = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+    for (int j = 0; j < 8; j += 2) rmax[i] = absmax3(rmax[i], v[i][j], v[i][j + 1]);
+  }
+  {
+    // over the 16 lanes of a row, the lanes sharing out the 4 rows: lane l ends
+    // with row 2 (l / 8) + l / 4 % 2
+    const float x0 = max_nan(l & 8 ? rmax[2] : rmax[0], __shfl_xor_sync(0xffffffffu, l & 8 ? rmax[0] : rmax[2], 8));
+    const float x1 = max_nan(l & 8 ? rmax[3] : rmax[1], __shfl_xor_sync(0xffffffffu, l & 8 ? rmax[1] : rmax[3], 8));
+    float m = max_nan(l & 4 ? x1 : x0, __shfl_xor_sync(0xffffffffu, l & 4 ? x0 : x1, 4));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    if ((l & 3) == 0) sh.rowmax[r0 + (l >> 3) * 2 + ((l >> 2) & 1)] = m;
+  }
+  if (!a.square && a.qt) {
+    float cm[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = __float_as_uint(v[i][j]) & 0x7fffffffu;
-      rmax[i] = max(rmax[i], b);
-      cmax[j] = max(cmax[j], b);
+    for (int j = 0; j < 8; ++j) cm[j] = absmax3(absmax3(0.f, v[0][j], v[1][j]), v[2][j], v[3][j]);
+    // the two halves of the warp (other rows, same columns) share out the columns
+    float o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = max_nan(half ? cm[4 + j] : cm[j], __shfl_xor_sync(0xffffffffu, half ? cm[j] : cm[4 + j], 16));
+    store4(&sh.colmax[warp][c0 + 4 * half], o);
+  }
+  __syncthreads();
+  next();
+  // a thread per row and per column: scale byte, its place, its inverse
+  const int t = threadIdx.x & 127, which = threadIdx.x >> 7;
+  if (which < 2) {
+    float m;
+    if (a.square) {
+      // magnitudes order like their bit patterns, NaN above all
+      m = max_nan(max_nan(sh.rowmax[lane], sh.rowmax[lane + 32]), max_nan(sh.rowmax[lane + 64], sh.rowmax[lane + 96]));
+      m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    } else if (which == 0) {
+      m = sh.rowmax[t];
+    } else {
+      m = 0.f;
+      if (a.qt) {
+#pragma unroll
+        for (int w = 0; w < 16; ++w) m = max_nan(m, sh.colmax[w][t]);
+      }
     }
-  if (a.square) {
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, rmax[i]);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) blockmax[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) m = max(m, blockmax[w]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) { rmax[i] = m; cmax[i] = m; }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) rmax[i] = max(rmax[i], __shfl_xor_sync(0xffffffffu, rmax[i], o));
-    if (a.qt) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t m = max(cmax[j], __shfl_xor_sync(0xffffffffu, cmax[j], 16));
-        if (half == 0) colmax[warp][c0 + j] = m;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) m = max(m, colmax[w][c0 + j]);
-        cmax[j] = m;
-      }
+    const uint32_t sb = scale_byte(__float_as_uint(m));
+    (which == 0 ? sh.rowinv : sh.colinv)[t] = scale_inv(sb);
+    // row r of x is row r of q, group cb; column c is row c of qt, group rb
+    uint8_t* s = which == 0 ? a.sc : a.sct;
+    if (which == 0 ? a.q != nullptr : a.qt != nullptr) {
+      const long long r = (which == 0 ? row0 : col0) + t, rows = which == 0 ? a.rows : a.cols;
+      const long long grp = which == 0 ? cb : rb, groups = which == 0 ? cblocks : (a.rows + 127) >> 7;
+      s += scale_offset(r, grp, (rows + 127) >> 7);
+      *s = r < rows ? (uint8_t)sb : 127;
+      if (grp == groups - 1)  // the groups that fill the last atom
+        for (int k = 1; k <= (int)((4 - (groups & 3)) & 3); ++k) s[k] = 127;
     }
   }
+  __syncthreads();
   if (a.q) {
-    const long long row_atoms = (a.rows + 127) >> 7;
-    const int last = cb == cblocks - 1 ? (4 - (cblocks & 3)) & 3 : 0;  // groups that fill the last atom
+    float inv[4];
+    load4(&sh.rowinv[r0], inv);
+    uint8_t* d = a.q + (row0 + r0) * a.ldq + col0 + c0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long r = row0 + r0 + i;
-      const uint32_t sb = scale_byte(rmax[i]);
-      if (l == 0) {
-        uint8_t* s = a.sc + scale_offset(r, cb, row_atoms);
-        *s = r < a.rows ? (uint8_t)sb : 127;
-        for (int k = 1; k <= last; ++k) s[k] = 127;
-      }
-      const float inv = scale_inv(sb);
+    for (int i = 0; i < 4; ++i, d += a.ldq) {
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) mul2(y[j], y[j + 1], v[i][j], v[i][j + 1], inv[i], inv[i]);
       uint2 o;
-      o.x = e4m3x2(v[i][0] * inv, v[i][1] * inv) | (e4m3x2(v[i][2] * inv, v[i][3] * inv) << 16);
-      o.y = e4m3x2(v[i][4] * inv, v[i][5] * inv) | (e4m3x2(v[i][6] * inv, v[i][7] * inv) << 16);
-      if (r >= a.rows) continue;
-      uint8_t* d = a.q + r * a.ldq + col0 + c0;
-      if (col0 + c0 + 8 <= a.cols) {
+      o.x = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
+      o.y = e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16);
+      if (!FULL && row0 + r0 + i >= a.rows) continue;
+      if (FULL || col0 + c0 + 8 <= a.cols) {
         *reinterpret_cast<uint2*>(d) = o;
       } else {
         for (int j = 0; j < 8; ++j)
@@ -155,37 +206,72 @@ __global__ void __launch_bounds__(256) fp8_block_quantize_kernel(const T* __rest
     }
   }
   if (a.qt) {
-    const long long col_atoms = (a.cols + 127) >> 7, rblocks = (a.rows + 127) >> 7;
-    const int last = rb == rblocks - 1 ? (int)((4 - (rblocks & 3)) & 3) : 0;
+    float inv[8];
+    load4(&sh.colinv[c0], *reinterpret_cast<float(*)[4]>(&inv[0]));
+    load4(&sh.colinv[c0 + 4], *reinterpret_cast<float(*)[4]>(&inv[4]));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t sb = scale_byte(cmax[j]);
-      const long long c = col0 + c0 + j;
-      if (warp == 0 && half == 0) {
-        uint8_t* s = a.sct + scale_offset(c, rb, col_atoms);
-        *s = c < a.cols ? (uint8_t)sb : 127;
-        for (int k = 1; k <= last; ++k) s[k] = 127;
-      }
-      const float inv = scale_inv(sb);
-      uint2 o;
-      o.x = e4m3x2(v[0][j] * inv, v[1][j] * inv) | (e4m3x2(v[2][j] * inv, v[3][j] * inv) << 16);
-      o.y = e4m3x2(v[4][j] * inv, v[5][j] * inv) | (e4m3x2(v[6][j] * inv, v[7][j] * inv) << 16);
-      tr[(c0 + j) * 16 + ((r0 >> 3) ^ l)] = o;
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) mul2(v[i][j], v[i][j + 1], v[i][j], v[i][j + 1], inv[j], inv[j + 1]);
+    uint32_t* trow = sh.tr + c0 * 32 + (slot ^ (2 * l));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) trow[j * 32] = e4m3x2(v[0][j], v[1][j]) | (e4m3x2(v[2][j], v[3][j]) << 16);
     __syncthreads();
+    uint8_t* d = a.qt + (col0 + slot) * a.ldqt + row0 + l * 8;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = k * 16 + (threadIdx.x >> 4), slot = threadIdx.x & 15;
-      const uint2 o = tr[c * 16 + (slot ^ (c >> 3))];
-      if (col0 + c >= a.cols) continue;
-      const long long r = row0 + slot * 8;
-      uint8_t* d = a.qt + (col0 + c) * a.ldqt + r;
-      if (r + 8 <= a.rows) {
+    for (int k = 0; k < 4; ++k, d += 32 * a.ldqt) {
+      const int c = k * 32 + slot;
+      const uint2 o = *reinterpret_cast<const uint2*>(&sh.tr[c * 32 + ((2 * l) ^ (2 * (c >> 3)))]);
+      if (!FULL && col0 + c >= a.cols) continue;
+      const long long r = row0 + l * 8;
+      if (FULL || r + 8 <= a.rows) {
         *reinterpret_cast<uint2*>(d) = o;
       } else {
         for (int j = 0; j < 8; ++j)
           if (r + j < a.rows) d[j] = (uint8_t)((j < 4 ? o.x : o.y) >> (8 * (j & 3)));
       }
     }
+  }
+}
+
+constexpr int QUANT_BLOCKS = 2;  // resident per SM
+// x's tile, then QuantShared
+template <typename T> constexpr int quant_smem() { return 128 * 128 * (int)sizeof(T) + (int)sizeof(QuantShared); }
+
+template <typename T, bool TMA>
+__global__ void __launch_bounds__(QUANT_THREADS, QUANT_BLOCKS)
+    fp8_block_quantize_kernel(const __grid_constant__ CUtensorMap map, const T* __restrict__ x, const QuantArgs a) {
+  pdl_wait();
+  extern __shared__ __align__(128) uint8_t quant_smem_raw[];
+  T* buf = reinterpret_cast<T*>(quant_smem_raw);
+  QuantShared& sh = *reinterpret_cast<QuantShared*>(quant_smem_raw + 128 * 128 * sizeof(T));
+  const int cblocks = (int)((a.cols + 127) >> 7);
+  auto fetch = [&](int tile) {
+    if (!TMA || threadIdx.x != 0 || tile >= a.tiles) return;
+    tc::mbar_expect_tx(&sh.full, 128 * 128 * sizeof(T));
+    tc::tma_load_2d(buf, &map, &sh.full, tile % cblocks * 128, tile / cblocks * 128);
+  };
+  if (TMA) {
+    if (threadIdx.x == 0) {
+      tc::mbar_init(&sh.full, 1);
+      sh.abort = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+  }
+  fetch(blockIdx.x);
+  uint32_t phase = 0;
+  for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    const long long rb = tile / cblocks;
+    const int cb = tile % cblocks;
+    auto next = [&] { fetch(tile + (int)gridDim.x); };
+    // a copy that never lands: reported, the codes are void, later waits return at once
+    if (TMA) tc::mbar_wait(&sh.full, phase, &sh.abort, a.err);
+    phase ^= 1;
+    if (rb * 128 + 128 <= a.rows && (long long)cb * 128 + 128 <= a.cols)
+      quantize_tile<true, TMA>(x, a, rb, cb, cblocks, sh, buf, next);
+    else
+      quantize_tile<false, TMA>(x, a, rb, cb, cblocks, sh, buf, next);
+    __syncthreads();  // the shared tables are free for the next tile
   }
 }

@@ -58,6 +58,26 @@ extern "C" int fp8_block_scale_bytes(long long rows, long long cols, size_t* byt
   return GPT_OK;
 }
 
+template <typename T>
+static int quantize_launch(const T* x, const QuantArgs& a, cudaStream_t st) {
+  const unsigned grid = (unsigned)std::min(a.tiles, QUANT_BLOCKS * device_sms());
+  CUtensorMap map = {};
+  ++g_launches;
+  if (!misaligned(x, 16) && (a.ldx * sizeof(T)) % 16 == 0) {
+    const uint64_t dims[2] = {(uint64_t)a.cols, (uint64_t)a.rows}, str[1] = {(uint64_t)a.ldx * sizeof(T)};
+    const uint32_t box[2] = {128, 128};
+    TRY(make_tmap_gen(&map, sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, x,
+                      dims, str, box, CU_TENSOR_MAP_SWIZZLE_NONE));
+    TRY(allow_smem(fp8_block_quantize_kernel<T, true>, quant_smem<T>()));
+    launch_pdl(fp8_block_quantize_kernel<T, true>, grid, QUANT_THREADS, quant_smem<T>(), st, map, x, a);
+  } else {
+    TRY(allow_smem(fp8_block_quantize_kernel<T, false>, quant_smem<T>()));
+    launch_pdl(fp8_block_quantize_kernel<T, false>, grid, QUANT_THREADS, quant_smem<T>(), st, map, x, a);
+  }
+  LAUNCH_CHECK();
+  return GPT_OK;
+}
+
 extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long long cols, long long ldx, int square,
                                   uint8_t* q, long long ldq, uint8_t* scales, uint8_t* qt, long long ldqt,
                                   uint8_t* scales_t, void* stream) {
@@ -76,15 +96,11 @@ extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long
   cudaStream_t st = (cudaStream_t)stream;
   ON_DEVICE_OF(fn, x);
   CHECK_PTR(fn, q); CHECK_PTR(fn, scales); CHECK_PTR(fn, qt); CHECK_PTR(fn, scales_t);
-  const int vec = !misaligned(x, 16) && (ldx * (long long)dtype_size(dtype)) % 16 == 0;
-  const QuantArgs a{rows, cols, ldx, q, ldq, scales, qt, ldqt, scales_t, square != 0, vec};
-  ++g_launches;
-  if (dtype == GPT_DTYPE_BF16)
-    launch_pdl(fp8_block_quantize_kernel<bf16>, (unsigned)tiles, 256, 0, st, (const bf16*)x, a);
-  else
-    launch_pdl(fp8_block_quantize_kernel<float>, (unsigned)tiles, 256, 0, st, (const float*)x, a);
-  LAUNCH_CHECK();
-  return GPT_OK;
+  unsigned* err = nullptr;
+  CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
+  const QuantArgs a{rows, cols, ldx, q, ldq, scales, qt, ldqt, scales_t, square != 0, (int)tiles, err};
+  if (dtype == GPT_DTYPE_BF16) return quantize_launch((const bf16*)x, a, st);
+  return quantize_launch((const float*)x, a, st);
 }
 
 // Tile shape and K split of a block-scaled product: pairs of SMs (256-row
