@@ -14,7 +14,7 @@
 // operations bound it.  fp32: the same pieces through plain FFMA products, with
 // fp32 logits of one piece at a time in the workspace.
 #pragma once
-#include "common.cuh"
+#include "gemm_tc.cuh"
 
 // (m, s) + (m2, s2) of sums s e^m; an empty part has m = -inf, s = 0
 __device__ __forceinline__ void lse_join(float& m, float& s, float m2, float s2) {
@@ -96,30 +96,37 @@ __global__ void __launch_bounds__(1024) ce_mean_kernel(const double2* __restrict
   }
 }
 
-// Gradient scale of every row: dtok[i], or dloss / count (dloss null: 1), 0 for
-// ignored rows.  Every block counts the targets itself (they are few and in
-// L2), so one launch does.
-__global__ void __launch_bounds__(1024) ce_row_scale_kernel(const int32_t* __restrict__ targets, int N, int V,
-                                                            const float* __restrict__ dloss,
-                                                            const float* __restrict__ dtok, float* __restrict__ g,
-                                                            unsigned* err) {
-  pdl_wait();
+// Gradient scale of a row: dtok[i], or base = dloss / count (dloss null: 1), 0
+// for ignored rows.  Every block counts the targets itself (they are few and
+// in L2), so that no launch has to come first.
+struct CeRowScale {
+  const int32_t* targets;
+  const float* dloss;
+  const float* dtok;
+  int N, V;
+  unsigned* err;
+};
+__device__ __forceinline__ float ce_scale_base(const CeRowScale& a) {
+  if (a.dtok) return 0.f;
   __shared__ int sh[32];
-  float base = 0.f;
-  if (!dtok) {
-    int c = 0;
-    for (int i = threadIdx.x; i < N; i += blockDim.x) { const int y = targets[i]; c += y >= 0 && y < V; }
-    c = __reduce_add_sync(0xffffffffu, c);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = c;
-    __syncthreads();
-    c = __reduce_add_sync(0xffffffffu, sh[threadIdx.x & 31]);
-    base = c > 0 ? (dloss ? *dloss : 1.f) / (float)c : 0.f;
-  }
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < N; i += gridDim.x * blockDim.x) {
-    const int y = targets[i];
-    if (y < -1 || y >= V) set_error(err, GPT_EBIT_INPUT);
-    g[i] = y >= 0 && y < V ? (dtok ? dtok[i] : base) : 0.f;
-  }
+  int c = 0;
+  for (int i = threadIdx.x; i < a.N; i += blockDim.x) { const int y = a.targets[i]; c += y >= 0 && y < a.V; }
+  c = __reduce_add_sync(0xffffffffu, c);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = c;
+  __syncthreads();
+  c = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) c += sh[w];
+  return c > 0 ? (a.dloss ? *a.dloss : 1.f) / (float)c : 0.f;
+}
+__device__ __forceinline__ float ce_row_scale(const CeRowScale& a, float base, int i) {
+  const int y = a.targets[i];
+  if (y < -1 || y >= a.V) set_error(a.err, GPT_EBIT_INPUT);
+  return y >= 0 && y < a.V ? (a.dtok ? a.dtok[i] : base) : 0.f;
+}
+__global__ void __launch_bounds__(1024) ce_row_scale_kernel(const CeRowScale a, float* __restrict__ g) {
+  pdl_wait();
+  const float base = ce_scale_base(a);
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.N; i += gridDim.x * blockDim.x) g[i] = ce_row_scale(a, base, i);
 }
 
 // ---------------------------------------------------------------- fp32 pieces
@@ -155,20 +162,121 @@ __global__ void __launch_bounds__(256) ce_piece_stats_kernel(const float* __rest
   }
 }
 
-// z -> dz in place
-__global__ void __launch_bounds__(256) ce_piece_grad_kernel(float* __restrict__ z, int width, int col0, float softcap,
-                                                            const int32_t* __restrict__ targets,
-                                                            const float* __restrict__ lse,
-                                                            const float* __restrict__ row_scale) {
+// fp32 products of the pieces (FFMA): C[m, n] = sum_k A[m, k] B[n, k].  32 x 32
+// tiles, so that the small decoders' products still make enough blocks; the 8
+// warps of a block take every eighth chunk of 16 k's each, through shared memory
+// of their own (no block barrier in the loop, the next chunk's loads in flight
+// meanwhile), 4 x 8 results per thread in packed pairs, and the partial tiles are
+// added in warp order.  FFMA bounds it at size; a small call is latency.
+struct CeProduct {
+  const float* A; long long lda; int a_kmajor;
+  const float* B; long long ldb; int b_kmajor;
+  float* C; long long ldc;
+  int M, N, K, beta, tiles;  // tiles = number of 32 x 32 tiles; 0: no product
+};
+// gradient epilogue (dz instead of z); lse null: none
+struct CeGrad {
+  const float* lse;
+  CeRowScale scale;
+  int col0;
+  float softcap;
+};
+constexpr int CEP_KC = 16, CEP_WARPS = 8;
+
+// row r, columns k0 ... of an operand (zeros beyond it)
+__device__ __forceinline__ void ce_load_chunk(float (&v)[CEP_KC], const float* __restrict__ p, long long ld, int kmajor,
+                                              int r, int rows, int k0, int K) {
+  if (kmajor) {
+    const float* q = p + r * ld + k0;
+    if (r < rows && k0 + CEP_KC <= K && ((ld & 3) | (reinterpret_cast<uintptr_t>(p) & 15)) == 0) {
+#pragma unroll
+      for (int k = 0; k < CEP_KC; k += 4) load4(q + k, *reinterpret_cast<float(*)[4]>(&v[k]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < CEP_KC; ++k) v[k] = r < rows && k0 + k < K ? q[k] : 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < CEP_KC; ++k) v[k] = r < rows && k0 + k < K ? p[(k0 + k) * ld + r] : 0.f;
+  }
+}
+
+// one or two products in one launch (dx and dW of a piece)
+__global__ void __launch_bounds__(CEP_WARPS * 32, 2) ce_product_kernel(const CeProduct p0, const CeProduct p1,
+                                                                    const CeGrad gr) {
   pdl_wait();
-  const long long row = blockIdx.x;
-  float* r = z + row * width;
-  const float l = lse[row], g = row_scale[row];
-  const int y = targets[row] - col0;
-  for (int i = threadIdx.x; i < width; i += blockDim.x) {
-    float v = r[i], slope = 1.f;
-    if (softcap > 0.f) { const float t = tanhf(v / softcap); v = softcap * t; slope = 1.f - t * t; }
-    r[i] = g != 0.f ? (expf(v - l) - (i == y ? 1.f : 0.f)) * slope * g : 0.f;
+  // per warp: its chunks of A and B; then its partial tile
+  __shared__ __align__(16) float sh[CEP_WARPS][2][CEP_KC][32];
+  const bool second = (int)blockIdx.x >= p0.tiles;
+  const CeProduct& p = second ? p1 : p0;
+  const int tile = blockIdx.x - (second ? p0.tiles : 0), nt = (p.N + 31) >> 5;
+  const int m0 = tile / nt * 32, n0 = tile % nt * 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tm = (lane >> 2) * 4, tn = (lane & 3) * 8;  // this thread's 4 x 8 results
+  float (&as)[CEP_KC][32] = sh[warp][0];
+  float (&bs)[CEP_KC][32] = sh[warp][1];
+  constexpr int STEP = CEP_WARPS * CEP_KC;
+  float acc[4][8] = {};
+  float va[CEP_KC], vb[CEP_KC];
+  int k0 = warp * CEP_KC;
+  const bool grad = gr.lse != nullptr && !second;
+  if (k0 < p.K) {
+    ce_load_chunk(va, p.A, p.lda, p.a_kmajor, m0 + lane, p.M, k0, p.K);
+    ce_load_chunk(vb, p.B, p.ldb, p.b_kmajor, n0 + lane, p.N, k0, p.K);
+  }
+  const float base = grad ? ce_scale_base(gr.scale) : 0.f;  // while the first chunk is on its way
+  for (; k0 < p.K; k0 += STEP) {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < CEP_KC; ++k) { as[k][lane] = va[k]; bs[k][lane] = vb[k]; }
+    __syncwarp();
+    if (k0 + STEP < p.K) {
+      ce_load_chunk(va, p.A, p.lda, p.a_kmajor, m0 + lane, p.M, k0 + STEP, p.K);
+      ce_load_chunk(vb, p.B, p.ldb, p.b_kmajor, n0 + lane, p.N, k0 + STEP, p.K);
+    }
+#pragma unroll 4
+    for (int k = 0; k < CEP_KC; ++k) {
+      float a[4], b[8];
+      load4(&as[k][tm], a);
+      load4(&bs[k][tn], *reinterpret_cast<float(*)[4]>(&b[0]));
+      load4(&bs[k][tn + 4], *reinterpret_cast<float(*)[4]>(&b[4]));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          tc::fma2v(acc[i][j], acc[i][j + 1], b[j], b[j + 1], a[i], acc[i][j], acc[i][j + 1]);
+    }
+  }
+  __syncwarp();
+  float* mine = &sh[warp][0][0][0] + tm * 32 + tn;  // partial tile [32][32]
+#pragma unroll
+  for (int i = 0; i < 4; ++i) { store4(mine + i * 32, &acc[i][0]); store4(mine + i * 32 + 4, &acc[i][4]); }
+  __syncthreads();
+  // four results per thread: row threadIdx / 8, four columns
+  const int m = m0 + (threadIdx.x >> 3), nc = (threadIdx.x & 7) * 4;
+  float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < CEP_WARPS; ++w) {
+    float v[4];
+    load4(&sh[w][0][0][0] + (threadIdx.x >> 3) * 32 + nc, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] += v[j];
+  }
+  if (m >= p.M) return;
+  const float l = grad ? gr.lse[m] : 0.f, g = grad ? ce_row_scale(gr.scale, base, m) : 0.f;
+  const int y = grad ? gr.scale.targets[m] - gr.col0 : -1;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = n0 + nc + j;
+    if (n >= p.N) continue;
+    float v = r[j];
+    if (grad) {  // (exp(z - lse) - [target]) * slope * scale; a row without a gradient stays out
+      float slope = 1.f;
+      if (gr.softcap > 0.f) { const float t = tanhf(v / gr.softcap); v = gr.softcap * t; slope = 1.f - t * t; }
+      v = g != 0.f ? (expf(v - l) - (n == y ? 1.f : 0.f)) * slope * g : 0.f;
+    }
+    float* c = p.C + m * p.ldc + n;
+    *c = (p.beta ? *c : 0.f) + v;
   }
 }
 

@@ -264,7 +264,7 @@ static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) 
     w.part = cv.take((size_t)cdiv(N, 32) * 16);
     if (!lp) w.dz = cv.take((size_t)N * w.piece * 4);
   } else {
-    w.rowg = cv.take((size_t)N * 4);
+    if (lp) w.rowg = cv.take((size_t)N * 4);
     w.dz = cv.take((size_t)N * (lp ? 64 * cdiv(w.piece, 64) : w.piece) * (lp ? 2 : 4));
     if (lp) {
       w.dx = cv.take((size_t)N * d * 4);
@@ -275,6 +275,17 @@ static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) 
   }
   w.total = cv.take(0);
   return w;
+}
+
+static CeProduct ce_product(const float* A, long long lda, int a_kmajor, const float* B, long long ldb, int b_kmajor,
+                            float* C, long long ldc, int M, int N, int K, int beta) {
+  return CeProduct{A, lda, a_kmajor, B, ldb, b_kmajor, C, ldc, M, N, K, beta, cdiv(M, 32) * cdiv(N, 32)};
+}
+static int ce_products(const CeProduct& p0, const CeProduct& p1, const CeGrad& gr, cudaStream_t st) {
+  ++g_launches;
+  launch_pdl(ce_product_kernel, p0.tiles + p1.tiles, CEP_WARPS * 32, 0, st, p0, p1, gr);
+  LAUNCH_CHECK();
+  return GPT_OK;
 }
 
 static int ce_check(const char* fn, const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V,
@@ -330,8 +341,9 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
     float* z = reinterpret_cast<float*>(b + p.dz);
     for (int v0 = 0; v0 < V; v0 += p.piece) {
       const int width = std::min(p.piece, V - v0);
-      TRY(gemm(g, N, width, d, op_k(x, ldx), op_k(static_cast<const float*>(w) + v0 * ldw, ldw),
-               epi(EPI_STORE_F32, z, width)));
+      TRY(ce_products(ce_product(static_cast<const float*>(x), ldx, 1, static_cast<const float*>(w) + v0 * ldw, ldw, 1, z,
+                                 width, N, width, d, 0),
+                      CeProduct{}, CeGrad{}, st));
       ++g_launches; launch_pdl(ce_piece_stats_kernel, N, 256, 0, st, (const float*)z, width, v0, v0 == 0 ? 1 : 0, softcap,
                                targets, N, stats, ztgt);
       LAUNCH_CHECK();
@@ -378,8 +390,11 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
   CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
   uint8_t* b = static_cast<uint8_t*>(workspace);
   float* rowg = reinterpret_cast<float*>(b + p.rowg);
-  ++g_launches; launch_pdl(ce_row_scale_kernel, std::min(32, cdiv(N, 1024)), 1024, 0, st, targets, N, V, dloss, dtok, rowg, err);
-  LAUNCH_CHECK();
+  const CeRowScale scale{targets, dloss, dtok, N, V, err};
+  if (lp) {
+    ++g_launches; launch_pdl(ce_row_scale_kernel, std::min(32, cdiv(N, 1024)), 1024, 0, st, scale, rowg);
+    LAUNCH_CHECK();
+  }
   const GemmCtx g{lp, reinterpret_cast<float*>(b + p.splitk), p.splitk_elems, err, st, nullptr};
   const size_t es = dtype_size(dtype);
   void* dz = b + p.dz;
@@ -395,9 +410,16 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
       e.softcap = softcap; e.targets = targets; e.col0 = v0; e.lse = lse; e.row_scale = rowg;
       TRY(gemm(g, N, width, d, op_k(x, ldx), op_k(wp, ldw), e));
     } else {
-      TRY(gemm(g, N, width, d, op_k(x, ldx), op_k(wp, ldw), epi(EPI_STORE_F32, dz, width)));
-      ++g_launches; launch_pdl(ce_piece_grad_kernel, N, 256, 0, st, (float*)dz, width, v0, softcap, targets, lse, (const float*)rowg);
-      LAUNCH_CHECK();
+      float* z = static_cast<float*>(dz);
+      const float* xf = static_cast<const float*>(x);
+      const float* wf = reinterpret_cast<const float*>(wp);
+      TRY(ce_products(ce_product(xf, ldx, 1, wf, ldw, 1, z, width, N, width, d, 0), CeProduct{},
+                      CeGrad{lse, scale, v0, softcap}, st));
+      CeProduct px = {}, pw = {};
+      if (dx) px = ce_product(z, width, 1, wf, ldw, 0, acc, ldacc, N, d, width, v0 > 0);
+      if (dw) pw = ce_product(z, width, 0, xf, ldx, 0, static_cast<float*>(dw) + v0 * lddw, lddw, width, d, N, dw_beta);
+      TRY(ce_products(px, pw, CeGrad{}, st));
+      continue;
     }
     if (dx) TRY(gemm(g, N, d, width, op_k(dz, ldz), op_mn(wp, ldw), epi(EPI_ACCUM_F32, acc, ldacc, v0 > 0), true));
     if (dw) {
