@@ -67,6 +67,7 @@ struct GemmEpilogue {
   const float* lse;
   const float* row_scale;
   int col0;
+  unsigned* counter;  // EPI_LSE: set to 0 (the next kernel's count of finished blocks)
 };
 
 template <typename act_t>

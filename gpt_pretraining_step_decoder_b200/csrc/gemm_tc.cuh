@@ -136,6 +136,8 @@ struct Params {
   // row atoms per k-quad
   CUtensorMap tm_sfa, tm_sfb;
   int a_atoms, b_atoms;
+  int n_run;   // K_LSE: column tiles in a row that one CTA (pair) takes of a row block
+  int a_skip;  // bytes of a stage's A tile that are not loaded (a product of fewer than 128 rows)
 };
 
 // ------------------------------------------------------------------ PTX helpers
@@ -525,6 +527,23 @@ __device__ __forceinline__ void tile_coords(int mn, const Params& p, int& mt, in
   nt = r / gsize;
 }
 
+// K_LSE walks the tiles in runs of n_run neighbouring column tiles of one row
+// block, so that a row's statistics stay in registers over the run and leave it
+// once (one pair per half tile and row cost a 2.5% longer loss at 32768 x 50304 x
+// 768: 103 MB written and read).  Index t of a unit's walk counts single tiles:
+// tile t % n_run of its run; the row block varies fastest over the runs, so the
+// units share the same columns of B.  False where a run ends past the last tile.
+__device__ __forceinline__ bool run_coords(int t, int unit, int n_units, const Params& p, int& mt, int& nt) {
+  const int item = unit + t / p.n_run * n_units;
+  mt = item % p.m_tiles;
+  nt = item / p.m_tiles * p.n_run + t % p.n_run;
+  return nt < p.n_tiles;
+}
+__device__ __forceinline__ int run_walk(int unit, int n_units, const Params& p) {
+  const int items = p.m_tiles * ((p.n_tiles + p.n_run - 1) / p.n_run);
+  return unit < items ? ((items - 1 - unit) / n_units + 1) * p.n_run : 0;
+}
+
 // byte offset of 16-byte chunk j of row r in a 128-byte-swizzled block
 // two fp32 lanes per instruction (sm_100 packed f32x2 arithmetic):
 // (y0, y1) = (x0, x1) * c + d
@@ -601,6 +620,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   static_assert((2 * C::STAGES + 4 + EPI_WARPS * C::NAUX) * 8 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if constexpr (KM == K_LSE)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.epi.counter = 0u;
   if constexpr (KM == K_QKV)
     if (threadIdx.x < 64 && p.epi.rope != nullptr) sturns[threadIdx.x] = p.epi.rope[threadIdx.x];
   const int per_product = p.m_tiles * p.n_tiles * p.splits;
@@ -608,6 +629,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // CTA pair: rank 0 issues the MMAs; tile t goes to pair blockIdx.x / CG
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
   const int unit = blockIdx.x / CG, n_units = gridDim.x / CG;
+  // this CTA's (pair's) walk over the tiles
+  constexpr bool RUNS = KM == K_LSE;
+  const int t_first = RUNS ? 0 : unit, t_step = RUNS ? 1 : n_units;
+  const int t_end = RUNS ? run_walk(unit, n_units, p) : tiles;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
@@ -649,13 +674,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool issued[C::STAGES];
       for (int s = 0; s < C::STAGES; ++s) issued[s] = false;
       bool ok = true;
-      for (int t = unit; t < tiles && ok; t += n_units) {
+      for (int t = t_first; t < t_end && ok; t += t_step) {
         const int z = B3 ? t / per_product : 0;
         const int tt = B3 ? t % per_product : t;
-        const int split = tt % p.splits;
+        const int split = RUNS ? 0 : tt % p.splits;
         const int mn = tt / p.splits;
         int mt, nt;
-        tile_coords(mn, p, mt, nt);
+        if constexpr (RUNS) {
+          if (!run_coords(t, unit, n_units, p, mt, nt)) continue;
+        } else {
+          tile_coords(mn, p, mt, nt);
+        }
         // this CTA's A rows and B rows of the tile
         const int m0 = (mt * CG + (int)rank) * BM, n0 = nt * BN + (int)rank * C::B_ROWS;
         const int kb0 = split * p.kb_per_split;
@@ -665,7 +694,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           // F8 = 2: the scale atoms of four k-blocks travel with the first (a
           // row atom past the end only scales rows past the end: clamped)
           const bool sf = F8 == 2 && (kb & 3) == 0;
-          const uint32_t bytes = C::STAGE_BYTES + (sf ? C::SF_BYTES : 0);
+          const uint32_t bytes = C::STAGE_BYTES + (sf ? C::SF_BYTES : 0) - (CG == 1 ? p.a_skip : 0);
           if constexpr (CG == 2) {
             // both CTAs' bytes complete on the even CTA's stage barrier, which
             // that CTA arms for the pair
@@ -726,8 +755,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int acc = 0;
       uint32_t acc_phase = 0;
       bool ok = true;
-      for (int t = unit; t < tiles && ok; t += n_units) {
-        const int split = (B3 ? t % per_product : t) % p.splits;
+      for (int t = t_first; t < t_end && ok; t += t_step) {
+        if constexpr (RUNS) {
+          int mt, nt;
+          if (!run_coords(t, unit, n_units, p, mt, nt)) continue;
+        }
+        const int split = RUNS ? 0 : (B3 ? t % per_product : t) % p.splits;
         const int kb0 = split * p.kb_per_split;
         const int kb1 = min(kb0 + p.kb_per_split, p.kb_total);
         // 192-column tiles start in the middle of a 128-row scale atom every other time
@@ -803,15 +836,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
+    float run_max = -INFINITY, run_sum = 0.f;  // K_LSE: the run so far
     // the accumulator-empty barrier lives in the even CTA of a pair
     const uint32_t tempty0 = CG == 2 ? mapa_shared(smem_u32(&tempty[0]), 0) : 0u;
-    for (int t = unit; t < tiles && ok; t += n_units) {
+    for (int t = t_first; t < t_end && ok; t += t_step) {
       const int z = B3 ? t / per_product : 0;
       const int tt = B3 ? t % per_product : t;
       const int split = tt % p.splits;
       const int mn = tt / p.splits;
       int mt, nt;
-      tile_coords(mn, p, mt, nt);
+      if constexpr (RUNS) {
+        if (!run_coords(t, unit, n_units, p, mt, nt)) continue;
+      } else {
+        tile_coords(mn, p, mt, nt);
+      }
       const int m0 = (mt * CG + (int)rank) * BM;  // this CTA's 128 accumulator rows
       const int n0 = nt * BN + ccol;  // first output column of this warp
       const int mrow0 = m0 + q * 32;
@@ -904,7 +942,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           add2(ps[(i >> 1) & 7], ps[((i >> 1) + 4) & 7], p0, p1);
         }
         rsum = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
-        if (nv > 0 && m < p.M) e.stats[(long long)(nt * 2 + (ew >> 2)) * p.M + m] = make_float2(rmax, rsum);
+        // join the run's earlier tiles; the run's last tile writes the pair
+        if (t % p.n_run != 0) {
+          const float mj = fmaxf(rmax, run_max);
+          if (mj != -INFINITY) {
+            rsum = rsum * __expf(rmax - mj) + run_sum * __expf(run_max - mj);
+            rmax = mj;
+          }
+        }
+        run_max = rmax;
+        run_sum = rsum;
+        if ((t + 1) % p.n_run == 0 || nt + 1 == p.n_tiles) {
+          if (m < p.M) e.stats[(long long)(nt / p.n_run * 2 + (ew >> 2)) * p.M + m] = make_float2(rmax, rsum);
+        }
       }
       if constexpr (KM == K_LOGITS) {
         // first pass over the accumulator: the half tile's row maximum, so

@@ -267,6 +267,12 @@ static int make_tmap3(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t 
   return make_tmap_gen(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, str, box);
 }
 
+// Column tiles per run of the cross entropy's statistics: 4 where that leaves
+// the units many runs each (their last wave is then a small part), else 1.
+static int lse_run(int M, int N, int BN, int cg) {
+  return (long long)cdiv(M, 128 * cg) * cdiv(N, BN) >= 128LL * (device_sms() / cg) ? 4 : 1;
+}
+
 template <int BN, int CG = 1>
 static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, GemmEpilogue e,
                           int splits, float* partial, unsigned* err, cudaStream_t st,
@@ -275,6 +281,9 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
   const bool b3 = bt.n > 1;
   if (b3 && (splits > 1 || (e.mode != EPI_STORE && e.mode != EPI_STORE_F32 && e.mode != EPI_AXPBY)))
     return fail(GPT_ERR_ARG, "batched GEMMs take store or AXPBY epilogues without split-K");
+  // a one-SM product of fewer than 128 rows loads only those of its A tile (in
+  // eights); what the tile's other rows hold reaches no stored result
+  const int a_rows = CG == 1 && !b3 && A.kmajor ? std::min(tc::BM, 8 * cdiv(M, 8)) : tc::BM;
   CUtensorMap ta, tb, tcm, taux;
   if (b3) {
     if (A.kmajor) TRY(make_tmap3(&ta, A.ptr, K, M, A.ld, bt.n, bt.sa, tc::BK, tc::BM));
@@ -282,7 +291,7 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
     if (B.kmajor) TRY(make_tmap3(&tb, B.ptr, K, N, B.ld, bt.n, bt.sb, tc::BK, BN / CG));
     else TRY(make_tmap3(&tb, B.ptr, N, K, B.ld, bt.n, bt.sb, 64, tc::BK));
   } else {
-    if (A.kmajor) TRY(make_tmap(&ta, A.ptr, K, M, A.ld, tc::BK, tc::BM));
+    if (A.kmajor) TRY(make_tmap(&ta, A.ptr, K, M, A.ld, tc::BK, a_rows));
     else TRY(make_tmap(&ta, A.ptr, M, K, A.ld, 64, tc::BK));
     // a CTA of a pair loads half of the tile's B rows
     if (B.kmajor) TRY(make_tmap(&tb, B.ptr, K, N, B.ld, tc::BK, BN / CG));
@@ -292,6 +301,8 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
   p.M = M; p.N = N; p.K = K;
   p.batch = bt.n;
   p.a_kmajor = A.kmajor; p.b_kmajor = B.kmajor;
+  p.a_skip = (tc::BM - a_rows) * tc::BK * 2;
+  p.n_run = e.mode == EPI_LSE ? lse_run(M, N, BN, CG) : 1;
   p.m_tiles = cdiv(M, CG * tc::BM);
   p.n_tiles = cdiv(N, BN);
   // n-fastest order while the whole B operand stays in L2; grouped m-blocks
@@ -407,6 +418,7 @@ static int gemm_f8_launch(int M, int N, int K, const uint8_t* A, long long lda, 
   }
   tc::Params p;
   p.M = M; p.N = N; p.K = K; p.batch = 1;
+  p.a_skip = 0; p.n_run = 1;
   p.a_kmajor = 1; p.b_kmajor = 1;
   p.m_tiles = cdiv(M, CG * tc::BM);
   p.n_tiles = cdiv(N, 256);
@@ -507,6 +519,15 @@ struct GemmCtx {
   Prof* prof;
 };
 
+// The cross entropy's products of one block of rows run on one SM per tile: a
+// pair's other half would idle (33 x 50304 x 768: 24.4 us on pairs, 19.3 on one SM).
+static bool ce_half_pair(int M) { return M <= 128; }
+// Pairs of statistics per row that an EPI_LSE product leaves (two per run of tiles).
+static int lse_pairs(int M, int N) {
+  const int cg = N >= 256 && gemm_pairs_enabled() && !ce_half_pair(M) ? 2 : 1, bn = N >= 256 ? 256 : 128;
+  return 2 * cdiv(cdiv(N, bn), lse_run(M, N, bn, cg));
+}
+
 static int gemm(const GemmCtx& g, int M, int N, int K, GemmOperand A, GemmOperand B, GemmEpilogue e,
                 bool allow_split = false, const char* label = "gemm") {
   if (M <= 0 || N <= 0 || K <= 0) return GPT_OK;
@@ -529,7 +550,8 @@ static int gemm(const GemmCtx& g, int M, int N, int K, GemmOperand A, GemmOperan
   // statistics and the ReLU^2 backward's activation stream), which measured
   // faster on one-SM tiles (B200: LM-head logits 2.55 vs 2.79 ms, ReLU^2
   // backward 2.04 vs 2.17 ms per GPT-2-small step)
-  if (N >= 256 && gemm_pairs_enabled() && e.mode != EPI_LOGITS && e.mode != EPI_DRELU2)
+  const bool half_pair = ce_half_pair(M) && (e.mode == EPI_LSE || e.mode == EPI_DLOGITS);
+  if (N >= 256 && gemm_pairs_enabled() && e.mode != EPI_LOGITS && e.mode != EPI_DRELU2 && !half_pair)
     return gemm_tc_launch<256, 2>(M, N, K, A, B, e, splits_for(256, 2), g.splitk, g.err, g.st);
   // one-CTA tiles: 256 wide (128 below 256 columns); fp32 outputs may take 192
   // when that fills the last wave of SMs better (N = 768: 4 x 192 instead of 3 x 256)
@@ -556,6 +578,7 @@ static GemmEpilogue epi(int mode, void* C, long long ldc, int beta = 0, void* C2
   e.aux_scale = 0.f;
   e.lse = e.row_scale = nullptr;
   e.col0 = 0;
+  e.counter = nullptr;
   e.T = e.H = e.qk_norm = 0; e.eps = 0.f;
   return e;
 }

@@ -32,67 +32,93 @@ __device__ __forceinline__ float ce_row_loss(float lse, float zt, int y, int V, 
   return valid ? lse - zt : 0.f;
 }
 
-// Block of 32 rows x 32 groups of half tiles; stats [n_tiles, N], so that a
-// warp reads 32 neighbouring rows.  Leaves each row's lse and loss, and the
-// block's loss sum (fp64) and count for ce_mean_kernel.
-__global__ void __launch_bounds__(1024) ce_combine_kernel(const float2* __restrict__ stats, int n_tiles, int N, int V,
-                                                          const int32_t* __restrict__ targets,
-                                                          const float* __restrict__ ztgt, float* __restrict__ lse_out,
-                                                          float* __restrict__ tok_loss, double2* __restrict__ part,
-                                                          unsigned* err) {
+// Block of 32 rows x G groups of pairs (a warp per group); stats [n_pairs, N],
+// so that a warp reads 32 neighbouring rows; G neighbouring lanes then join the
+// groups of one row.  Leaves each row's lse and loss and the block's loss sum
+// (fp64) and count; the block that finishes last (`counter`, zeroed by the kernel
+// before) adds those in block order and writes the mean.  G = 32 for few rows
+// (latency: all pairs in flight at once), 8 for many (more blocks per SM hide
+// it: 32768 rows of 100 pairs took 41 us with G = 32).
+template <int G>
+__global__ void __launch_bounds__(32 * G) ce_combine_kernel(const float2* __restrict__ stats, int n_tiles, int N, int V,
+                                                            const int32_t* __restrict__ targets,
+                                                            const float* __restrict__ ztgt, float* __restrict__ lse_out,
+                                                            float* __restrict__ tok_loss, double2* __restrict__ part,
+                                                            unsigned* __restrict__ counter, float* __restrict__ loss,
+                                                            unsigned* err) {
   pdl_wait();
-  __shared__ float2 sh[32][33];
+  __shared__ float2 sh[G][33];
+  __shared__ double sums[2][32];
+  __shared__ int last;
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + lane;
+  const int r = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
-  if (row < N) {
-    constexpr int U = 4;  // pairs in flight per thread
-    for (int j = grp; j < n_tiles; j += 32 * U) {
+  if (r < N) {
+    constexpr int U = 16;  // pairs in flight per thread, joined at once
+    for (int j = grp; j < n_tiles; j += G * U) {
       float2 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        v[u] = j + 32 * u < n_tiles ? stats[(long long)(j + 32 * u) * N + row] : make_float2(-INFINITY, 0.f);
+        v[u] = j + G * u < n_tiles ? __ldcg(stats + (long long)(j + G * u) * N + r) : make_float2(-INFINITY, 0.f);
+      float mx = m;
 #pragma unroll
-      for (int u = 0; u < U; ++u) lse_join(m, s, v[u].x, v[u].y);
+      for (int u = 0; u < U; ++u) mx = fmaxf(mx, v[u].x);
+      const float ref = mx == -INFINITY ? 0.f : mx;  // nothing but empty parts: their sums are 0 (or NaN, which stays)
+      s *= __expf(m - ref);
+#pragma unroll
+      for (int u = 0; u < U; ++u) s += v[u].y * __expf(v[u].x - ref);
+      m = mx;
     }
   }
   sh[grp][lane] = make_float2(m, s);
   __syncthreads();
-  if (grp == 0) {
-    for (int g = 1; g < 32; ++g) lse_join(m, s, sh[g][lane].x, sh[g][lane].y);
-    double l = 0.0;
+  const int br = threadIdx.x / G, row = blockIdx.x * 32 + br, g = threadIdx.x % G;
+  m = sh[g][br].x;
+  s = sh[g][br].y;
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1)
+    lse_join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+  if (g == 0) {
     int valid = 0;
+    float t = 0.f;
     if (row < N) {
       const float lse = m + logf(s);
       const int y = targets[row];
-      const float t = ce_row_loss(lse, y >= 0 && y < V ? ztgt[row] : 0.f, y, V, valid, err);
+      t = ce_row_loss(lse, y >= 0 && y < V ? ztgt[row] : 0.f, y, V, valid, err);
       if (lse_out) lse_out[row] = lse;
       if (tok_loss) tok_loss[row] = t;
-      l = t;
     }
-    l = warp_sum_d(l);
-    const int c = __reduce_add_sync(0xffffffffu, valid);
-    if (lane == 0) part[blockIdx.x] = make_double2(l, (double)c);
+    sums[0][br] = t;
+    sums[1][br] = valid;
   }
-}
-
-// mean of the valid rows' losses, the blocks' sums added in a fixed order
-__global__ void __launch_bounds__(1024) ce_mean_kernel(const double2* __restrict__ part, int parts,
-                                                       float* __restrict__ loss, unsigned* err) {
-  pdl_wait();
-  __shared__ double sh[2][32];
+  __syncthreads();
+  if (grp == 0) {
+    const double l = warp_sum_d(sums[0][lane]), c = warp_sum_d(sums[1][lane]);
+    if (lane == 0) {
+      part[blockIdx.x] = make_double2(l, c);
+      __threadfence();
+      last = atomicAdd(counter, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
   double l = 0.0, c = 0.0;
-  for (int i = threadIdx.x; i < parts; i += blockDim.x) { const double2 p = part[i]; l += p.x; c += p.y; }
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += blockDim.x) {
+    const double2 p = __ldcg(part + i);
+    l += p.x;
+    c += p.y;
+  }
   l = warp_sum_d(l);
   c = warp_sum_d(c);
-  if ((threadIdx.x & 31) == 0) { sh[0][threadIdx.x >> 5] = l; sh[1][threadIdx.x >> 5] = c; }
+  if (lane == 0) { sums[0][grp] = l; sums[1][grp] = c; }
   __syncthreads();
   if (threadIdx.x == 0) {
     l = c = 0.0;
-    for (int w = 0; w < 32; ++w) { l += sh[0][w]; c += sh[1][w]; }
-    const float r = c > 0.0 ? (float)(l / c) : 0.f;
-    if (!isfinite(r)) set_error(err, GPT_EBIT_NONFINITE);
-    if (loss) *loss = r;
+    for (int w = 0; w < G; ++w) { l += sums[0][w]; c += sums[1][w]; }
+    const float mean = c > 0.0 ? (float)(l / c) : 0.f;
+    if (!isfinite(mean)) set_error(err, GPT_EBIT_NONFINITE);
+    if (loss) *loss = mean;
   }
 }
 
@@ -135,8 +161,10 @@ __global__ void __launch_bounds__(1024) ce_row_scale_kernel(const CeRowScale a, 
 // first: the row's pair starts here.
 __global__ void __launch_bounds__(256) ce_piece_stats_kernel(const float* __restrict__ z, int width, int col0, int first,
                                                              float softcap, const int32_t* __restrict__ targets, int N,
-                                                             float2* __restrict__ stats, float* __restrict__ ztgt) {
+                                                             float2* __restrict__ stats, float* __restrict__ ztgt,
+                                                             unsigned* __restrict__ counter) {
   pdl_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0u;
   __shared__ float sh[32];
   const long long row = blockIdx.x;
   const float* r = z + row * width;

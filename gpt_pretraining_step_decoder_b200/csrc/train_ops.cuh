@@ -148,6 +148,7 @@ static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda,
   TRY(make_tmap_gen(&p.tm_sfa, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sa, dsa, ls, bsa, CU_TENSOR_MAP_SWIZZLE_NONE));
   TRY(make_tmap_gen(&p.tm_sfb, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sb, dsb, ls, bsb, CU_TENSOR_MAP_SWIZZLE_NONE));
   p.a_atoms = cdiv(M, 128); p.b_atoms = cdiv(N, 128);
+  p.a_skip = 0; p.n_run = 1;
   p.M = M; p.N = N; p.K = K; p.batch = 1;
   p.a_kmajor = 1; p.b_kmajor = 1;
   p.m_tiles = cdiv(M, CG * tc::BM);
@@ -248,7 +249,7 @@ static int ce_piece(int N, int V, int d, int dtype, int asked) {
 
 // Byte offsets of the operator's scratch inside the caller's workspace.
 struct CeWs {
-  size_t stats, ztgt, part, rowg, dz, dx, splitk, total;
+  size_t stats, ztgt, part, counter, rowg, dz, dx, splitk, total;
   int piece, n_tiles;
   long long splitk_elems;
 };
@@ -258,10 +259,12 @@ static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) 
   const bool lp = dtype == GPT_DTYPE_BF16;
   w.piece = ce_piece(N, V, d, dtype, asked);
   if (!backward) {
-    w.n_tiles = lp ? cdiv(V, V >= 256 ? 128 : 64) : 1;
-    w.stats = cv.take((size_t)w.n_tiles * N * 8);
+    w.n_tiles = lp ? lse_pairs(N, V) : 1;
+    // room for either tile shape, whichever is set when the call comes
+    w.stats = cv.take((size_t)(lp ? 2 * cdiv(V, V >= 256 ? 256 : 128) : 1) * N * 8);
     w.ztgt = cv.take((size_t)N * 4);
     w.part = cv.take((size_t)cdiv(N, 32) * 16);
+    w.counter = cv.take(4);
     if (!lp) w.dz = cv.take((size_t)N * w.piece * 4);
   } else {
     if (lp) w.rowg = cv.take((size_t)N * 4);
@@ -332,10 +335,11 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
   float2* stats = reinterpret_cast<float2*>(b + p.stats);
   float* ztgt = reinterpret_cast<float*>(b + p.ztgt);
   double2* part = reinterpret_cast<double2*>(b + p.part);
+  unsigned* counter = reinterpret_cast<unsigned*>(b + p.counter);
   const GemmCtx g{dtype == GPT_DTYPE_BF16, nullptr, 0, err, st, nullptr};
   if (g.bf16) {
     GemmEpilogue e = epi(EPI_LSE, nullptr, V);
-    e.softcap = softcap; e.stats = stats; e.targets = targets; e.ztgt = ztgt;
+    e.softcap = softcap; e.stats = stats; e.targets = targets; e.ztgt = ztgt; e.counter = counter;
     TRY(gemm(g, N, V, d, op_k(x, ldx), op_k(w, ldw), e));
   } else {
     float* z = reinterpret_cast<float*>(b + p.dz);
@@ -345,15 +349,15 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
                                  width, N, width, d, 0),
                       CeProduct{}, CeGrad{}, st));
       ++g_launches; launch_pdl(ce_piece_stats_kernel, N, 256, 0, st, (const float*)z, width, v0, v0 == 0 ? 1 : 0, softcap,
-                               targets, N, stats, ztgt);
+                               targets, N, stats, ztgt, counter);
       LAUNCH_CHECK();
     }
   }
   const int blocks = cdiv(N, 32);
-  ++g_launches; launch_pdl(ce_combine_kernel, blocks, 1024, 0, st, (const float2*)stats, p.n_tiles, N, V, targets,
-                           (const float*)ztgt, lse, tok_loss, part, err);
-  LAUNCH_CHECK();
-  ++g_launches; launch_pdl(ce_mean_kernel, 1, 1024, 0, st, (const double2*)part, blocks, loss, err);
+  const bool few = blocks <= device_sms();
+  ++g_launches; launch_pdl(few ? ce_combine_kernel<32> : ce_combine_kernel<8>, blocks, few ? 1024 : 256, 0, st,
+                           (const float2*)stats, p.n_tiles, N, V, targets, (const float*)ztgt, lse, tok_loss, part,
+                           counter, loss, err);
   LAUNCH_CHECK();
   return GPT_OK;
 }
