@@ -7,6 +7,7 @@ name CUDA streams.  Importing this package raises if the compiled library is
 missing: there is no fallback path.
 """
 
+import array
 import ctypes
 import os
 
@@ -409,28 +410,32 @@ def grad_clip_workspace_bytes(n):
     return b.value
 
 
+_clip_codes = None  # torch element type -> DTYPE_*
+
+
 def grad_clip(grads, outs, max_norm, norm_out, workspace, ws_bytes, stream=None):
     """Global L2 norm of a list of contiguous fp32 / bf16 CUDA tensors into
     norm_out (device float, or None), and the tensors scaled by min(1, max_norm /
     (norm + 1e-6)): in place (outs None) or into the tensors of outs, which
     have the same sizes and types.  max_norm = 0: no scaling."""
-    import torch
-    n = len(grads)
-    codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
-    for i, t in enumerate(grads):
-        o = t if outs is None else outs[i]
-        if t.dtype not in codes or not t.is_contiguous():
-            raise ValueError(f"grad_clip: tensor {i}: a contiguous fp32 or bf16 tensor is wanted")
-        if o is not t and (o.dtype != t.dtype or o.numel() != t.numel() or not o.is_contiguous()):
-            raise ValueError(f"grad_clip: output {i} differs from its tensor in type or size, or is not contiguous")
-    if outs is not None and len(outs) != n:
-        raise ValueError("grad_clip: as many outputs as tensors are wanted")
-    ptrs = (_P * n)(*[t.data_ptr() for t in grads])
-    out_ptrs = None if outs is None else (_P * n)(*[t.data_ptr() for t in outs])
-    sizes = (_LL * n)(*[t.numel() for t in grads])
-    dtypes = (_I * n)(*[codes[t.dtype] for t in grads])
-    return _check(_lib.grad_clip(n, ptrs, out_ptrs, sizes, dtypes, float(max_norm), _ptr(norm_out), _ptr(workspace),
-                                 ws_bytes, _stream(stream)), "grad_clip")
+    global _clip_codes
+    if _clip_codes is None:
+        import torch
+        _clip_codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
+    types, sizes = [t.dtype for t in grads], [t.numel() for t in grads]
+    if not all([t.is_contiguous() for t in grads]) or not _clip_codes.keys() >= set(types):
+        raise ValueError("grad_clip: contiguous fp32 or bf16 tensors are wanted")
+    out_ptrs = None
+    if outs is not None:
+        if ([t.dtype for t in outs] != types or [t.numel() for t in outs] != sizes or
+                not all([t.is_contiguous() for t in outs])):
+            raise ValueError("grad_clip: the outputs differ from their tensors in number, type or size, or are not contiguous")
+        out_ptrs = array.array("Q", [t.data_ptr() for t in outs])
+    ptrs, ns = array.array("Q", [t.data_ptr() for t in grads]), array.array("q", sizes)
+    codes = array.array("i", [_clip_codes[t] for t in types])
+    return _check(_lib.grad_clip(len(sizes), ptrs.buffer_info()[0], None if outs is None else out_ptrs.buffer_info()[0],
+                                 ns.buffer_info()[0], codes.buffer_info()[0], float(max_norm), _ptr(norm_out),
+                                 _ptr(workspace), ws_bytes, _stream(stream)), "grad_clip")
 
 
 def gptx_set_gemm_cta_pairs(on):

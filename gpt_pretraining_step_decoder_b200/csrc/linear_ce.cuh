@@ -52,6 +52,13 @@ __global__ void __launch_bounds__(32 * G) ce_combine_kernel(const float2* __rest
   __shared__ int last;
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int r = blockIdx.x * 32 + lane;
+  const int br = threadIdx.x / G, row = blockIdx.x * 32 + br, g = threadIdx.x % G;  // the row that is joined below
+  int y = -1;
+  float zt = 0.f;
+  if (g == 0 && row < N) {
+    y = targets[row];
+    zt = ztgt[row];  // written only where the target is one
+  }
   float m = -INFINITY, s = 0.f;
   if (r < N) {
     constexpr int U = 16;  // pairs in flight per thread, joined at once
@@ -72,7 +79,6 @@ __global__ void __launch_bounds__(32 * G) ce_combine_kernel(const float2* __rest
   }
   sh[grp][lane] = make_float2(m, s);
   __syncthreads();
-  const int br = threadIdx.x / G, row = blockIdx.x * 32 + br, g = threadIdx.x % G;
   m = sh[g][br].x;
   s = sh[g][br].y;
 #pragma unroll
@@ -83,8 +89,7 @@ __global__ void __launch_bounds__(32 * G) ce_combine_kernel(const float2* __rest
     float t = 0.f;
     if (row < N) {
       const float lse = m + logf(s);
-      const int y = targets[row];
-      t = ce_row_loss(lse, y >= 0 && y < V ? ztgt[row] : 0.f, y, V, valid, err);
+      t = ce_row_loss(lse, zt, y, V, valid, err);
       if (lse_out) lse_out[row] = lse;
       if (tok_loss) tok_loss[row] = t;
     }
