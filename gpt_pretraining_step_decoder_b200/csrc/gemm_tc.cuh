@@ -49,9 +49,12 @@
 // producer loads the atoms with every fourth k-block, the MMA warp copies them
 // to tensor memory ahead of that block's products (copies and products of one
 // thread execute in order), and the accumulator comes out fully scaled, so the
-// mainloop and the epilogues are those of the unscaled form.  Tiles are 192 or
-// 128 columns wide: two 256-column accumulators would leave no tensor memory
-// for the scales.
+// mainloop and the epilogues are those of the unscaled form.  Two 256-column
+// accumulators would leave no tensor memory for the scales: 256-column tiles
+// have one, which the epilogue hands back as soon as it holds the values in
+// registers, 128-column tiles two.  (192-column tiles with two accumulators lose:
+// L2 to shared memory bounds the e4m3 products, about 10 TB/s over the GPU, and
+// they need 17% more bytes per product.)
 //
 // K-major and MN-major operands are both read straight from their
 // row-major buffers (the UMMA descriptor's major-ness bit), so forward,
@@ -111,7 +114,8 @@ template <int BN, int HEAVY, int CG = 1, int SF = 0> struct Cfg {
   static constexpr int TMEM_COLS = (2 * BN <= 256 && !SF) ? 256 : 512;  // two accumulators, power of two
   static constexpr int SFB_ATOMS = SF ? (BN + 127) / 128 : 0;
   static constexpr int SF_BYTES = SF ? 512 * (1 + SFB_ATOMS) : 0;
-  static_assert(!SF || 2 * BN + 2 * 4 * (1 + SFB_ATOMS) <= 512, "accumulators and scales share TMEM");
+  static constexpr int NACC = SF && BN == 256 ? 1 : 2;  // accumulators
+  static_assert(!SF || NACC * BN + 2 * 4 * (1 + SFB_ATOMS) <= 512, "accumulators and scales share TMEM");
   static constexpr int NSTG = HEAVY ? 0 : 1;           // staging blocks per epilogue warp
   static constexpr int NAUX = 2;                       // activation blocks per epilogue warp (ReLU^2 bwd)
   static constexpr int AUX = HEAVY ? NAUX * 32 * 128 : 0;  // activation bytes per epilogue warp
@@ -575,8 +579,6 @@ __device__ __forceinline__ void mulsub2(float& y0, float& y1, float p0, float p1
       : "=f"(y0), "=f"(y1)
       : "f"(x0), "f"(x1), "f"(d0), "f"(d1), "f"(p0), "f"(p1));
 }
-// the same for 64-byte rows (64-byte swizzle)
-__device__ __forceinline__ uint32_t swz64(int r, int j) { return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)); }
 __device__ __forceinline__ uint32_t swz128(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
 
 // cos and sin of the RoPE angle t theta_f from the frequency's turns per
@@ -763,13 +765,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int split = RUNS ? 0 : (B3 ? t % per_product : t) % p.splits;
         const int kb0 = split * p.kb_per_split;
         const int kb1 = min(kb0 + p.kb_per_split, p.kb_total);
-        // 192-column tiles start in the middle of a 128-row scale atom every other time
-        uint32_t sfb_shift = 0;
-        if constexpr (F8 == 2 && BN % 128 != 0) {
-          int mt, nt;
-          tile_coords(t / p.splits, p, mt, nt);
-          sfb_shift = (uint32_t)(nt * BN % 128) / 32;
-        }
         if (!warp_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.err)) { ok = false; break; }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
@@ -782,13 +777,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if constexpr (F8 == 2) {
             if ((kb & 3) == 0) {
               sf_buf ^= 1u;
-              const uint32_t t0 = tmem_base + 2 * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
+              const uint32_t t0 = tmem_base + C::NACC * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
               const uint32_t s0 = smem_u32(sSF + stage * C::SF_BYTES);
 #pragma unroll
               for (int a = 0; a < 1 + C::SFB_ATOMS; ++a) tc_copy_scales_w<CG>(t0 + 4 * a, scale_desc(s0 + 512 * a));
             }
-            sfa = tmem_base + 2 * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
-            sfb = sfa + 4 + sfb_shift;
+            sfa = tmem_base + C::NACC * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
+            sfb = sfa + 4;
             sid = (uint32_t)(kb & 3);
           }
 #pragma unroll
@@ -809,7 +804,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         if constexpr (CG == 2) tc_commit_pair_w(&tfull[acc]);
         else tc_commit_w(&tfull[acc]);
-        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+        if (++acc == C::NACC) { acc = 0; acc_phase ^= 1; }
       }
     }
   } else {
@@ -829,9 +824,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if constexpr (F8 == 1) ealpha *= (e.scale_a ? *e.scale_a : 1.f) * (e.scale_b ? *e.scale_b : 1.f);
     constexpr bool f32out = KM == K_STORE_F32 || KM == K_REDUCE_F32 || KM == K_PARTIAL;
     constexpr bool has_aux = KM == K_DRELU2 || KM == K_AXPBY;
-    // columns per staging row: 128 bytes, or 64 where a bf16 half tile is no multiple of 64 columns
-    constexpr bool narrow = F8 == 2 && !f32out && HALF % 64 != 0;
-    constexpr int CW = f32out || narrow ? 32 : 64;
+    constexpr int CW = f32out ? 32 : 64;  // columns per 128-byte staging row
     static_assert(!has_aux || HALF / CW <= C::NAUX, "one activation block per column block");
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -1182,7 +1175,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
         } else {
 #pragma unroll
-          for (int j = 0; j < CW / 8; ++j) {
+          for (int j = 0; j < 8; ++j) {
             uint4 o;
             __nv_bfloat162 b0 = __floats2bfloat162_rn(v[8 * j], v[8 * j + 1]);
             __nv_bfloat162 b1 = __floats2bfloat162_rn(v[8 * j + 2], v[8 * j + 3]);
@@ -1192,7 +1185,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             o.y = *reinterpret_cast<uint32_t*>(&b1);
             o.z = *reinterpret_cast<uint32_t*>(&b2);
             o.w = *reinterpret_cast<uint32_t*>(&b3);
-            *reinterpret_cast<uint4*>(stg + (narrow ? swz64(lane, j) : swz128(lane, j))) = o;
+            *reinterpret_cast<uint4*>(stg + swz128(lane, j)) = o;
           }
         }
         fence_async_smem();
@@ -1247,7 +1240,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           else mbar_arrive(&tempty[acc]);
         }
       }
-      if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+      if (++acc == C::NACC) { acc = 0; acc_phase ^= 1; }
     }
     if (lane == 0) bulk_wait0();  // all of this warp's stores are complete
     if (has_aux && lane == 0) {

@@ -104,7 +104,7 @@ extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long
 }
 
 // Tile shape and K split of a block-scaled product: pairs of SMs (256-row
-// tiles) where there is more than one block of 128 rows, and the width (192 or
+// tiles) where there is more than one block of 128 rows, and the width (256 or
 // 128 columns) and split with the least estimated time, in SM cycles: whole
 // waves of tiles, each k-block the longer of its MMAs and of its operands' way
 // from L2 (about 64 bytes a cycle and SM), plus the tile's start and epilogue;
@@ -116,8 +116,8 @@ static F8bPlan f8b_plan(int M, int N, int K) {
   const int quads = cdiv(K, 512), units = device_sms() / cg;
   F8bPlan best{128, cg, 1};
   double best_t = 1e300;
-  for (int bn : {192, 128}) {
-    if (bn == 192 && (cg == 1 || N <= 128)) continue;
+  for (int bn : {256, 128}) {
+    if (bn == 256 && N <= 128) continue;
     const double kb_cycles = std::max(2.0 * bn, (128 + bn / cg) * 128 / 64.0);
     const long long tiles = (long long)cdiv(M, 128 * cg) * cdiv(N, bn);
     for (int s = 1; s <= (N % 4 == 0 && tiles < units ? std::min(32, quads) : 1); ++s) {
@@ -172,11 +172,8 @@ static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda,
     return GPT_OK;
   }
   const uint64_t dims[2] = {(uint64_t)N, (uint64_t)M}, str[1] = {(uint64_t)e.ldc * (f32 ? 4 : 2)};
-  // bf16 half tiles of 96 columns go out in 32-column blocks (64-byte rows)
-  constexpr bool narrow = (BN / 2) % 64 != 0;
-  const uint32_t box[2] = {f32 || narrow ? 32u : 64u, 32};
-  TRY(make_tmap_gen(&tcm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, e.C, dims, str, box,
-                    f32 || !narrow ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B));
+  const uint32_t box[2] = {f32 ? 32u : 64u, 32};
+  TRY(make_tmap_gen(&tcm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, e.C, dims, str, box));
   if (!f32) return gemm_tc_launch_k<BN, tc::K_STORE, CG, 2>(ta, tb, tcm, tcm, p, st);
   if (e.beta) return gemm_tc_launch_k<BN, tc::K_REDUCE_F32, CG, 2>(ta, tb, tcm, tcm, p, st);
   return gemm_tc_launch_k<BN, tc::K_STORE_F32, CG, 2>(ta, tb, tcm, tcm, p, st);
@@ -213,9 +210,11 @@ extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long l
   CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
   const GemmEpilogue e = epi(out_dtype == GPT_DTYPE_BF16 ? EPI_STORE : EPI_ACCUM_F32, C, ldc, beta != 0);
   float* part = static_cast<float*>(workspace);
-  if (pl.bn == 192) return gemm_f8b_launch<192, 2>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
-  if (pl.cg == 2) return gemm_f8b_launch<128, 2>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
-  return gemm_f8b_launch<128, 1>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st);
+#define F8B(BN, CG) \
+  gemm_f8b_launch<BN, CG>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st)
+  if (pl.bn == 256) return pl.cg == 2 ? F8B(256, 2) : F8B(256, 1);
+  return pl.cg == 2 ? F8B(128, 2) : F8B(128, 1);
+#undef F8B
 }
 
 // ======================================================================== cross entropy without stored logits
