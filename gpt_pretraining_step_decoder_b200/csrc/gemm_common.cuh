@@ -30,7 +30,7 @@ enum EpiMode {
                       // the value-table row; C(act) = result
   EPI_LSE = 8,        // no output: per (column half tile, row) m = max z and s = sum exp(z - m),
                       // z = softcap(acc), into stats; z at the row's target column into ztgt
-  EPI_DLOGITS = 9,    // C(bf16) = (exp(z - lse) - [column = target]) * row_scale, times the
+  EPI_DLOGITS = 9,    // C(bf16) = (exp(z - lse) - [column = target]) * row gradient, times the
                       // softcap's slope 1 - (z / softcap)^2 (tensor-core path only, as the former)
   EPI_AXPBY = 7,      // C(act) = alpha * acc + aux_scale * aux(act), aux of C's shape and ld
                       // (the Newton-Schulz polynomial's combinations; tensor-core path)
@@ -58,15 +58,20 @@ struct GemmEpilogue {
   const int32_t* rv;
   int T, H, qk_norm;
   float eps;
-  // FP8 path: acc is further multiplied by *scale_a * *scale_b (device scalars; null = 1)
+  // store, fp32 and split-K epilogues: acc is further multiplied by *scale_a * *scale_b
+  // (device scalars; null = 1)
   const float* scale_a;
   const float* scale_b;
   float aux_scale;  // EPI_AXPBY
-  // EPI_DLOGITS: log-sum-exp and gradient scale per row; columns are those of
-  // a piece of the vocabulary that starts at col0 (targets count from 0)
+  // EPI_DLOGITS: log-sum-exp per row, gradient of the row's loss (null: 1 for
+  // every target in [0, vocab), scaled by the products that follow); columns
+  // are those of a piece of the vocabulary that starts at col0.  base_out (null:
+  // none): receives dloss / number of targets in [0, vocab) (dloss null: 1)
   const float* lse;
-  const float* row_scale;
-  int col0;
+  const float* dtok;
+  const float* dloss;
+  float* base_out;
+  int vocab, col0;
   unsigned* counter;  // EPI_LSE: set to 0 (the next kernel's count of finished blocks)
 };
 
@@ -109,7 +114,8 @@ __global__ void splitk_reduce_kernel(const float* __restrict__ part, int S, int 
                                      GemmEpilogue e) {
   pdl_wait();     // the previous kernel in the stream has completed (programmatic launch)
   const long long total = (long long)M * N;
-  const bool vec = (N % 4) == 0 && (e.ldc % 4) == 0 && (e.mode == EPI_ACCUM_F32 || e.mode == EPI_STORE_F32);
+  const bool lp_out = e.mode == EPI_STORE && sizeof(act_t) == 2;
+  const bool vec = (N % 4) == 0 && (e.ldc % 4) == 0 && (e.mode == EPI_ACCUM_F32 || e.mode == EPI_STORE_F32 || lp_out);
   if (vec) {
     // four consecutive columns of one row per thread (same sum order per element)
     const long long total4 = total / 4;
@@ -121,6 +127,11 @@ __global__ void splitk_reduce_kernel(const float* __restrict__ part, int S, int 
         acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
       }
       const long long i = i4 * 4, m = i / N, n = i % N;
+      if (lp_out) {
+        const float r[4] = {acc.x * e.alpha, acc.y * e.alpha, acc.z * e.alpha, acc.w * e.alpha};
+        store4(reinterpret_cast<act_t*>(e.C) + m * e.ldc + n, r);
+        continue;
+      }
       float4* c = reinterpret_cast<float4*>(reinterpret_cast<float*>(e.C) + m * e.ldc + n);
       if (e.mode == EPI_ACCUM_F32 && e.beta) {
         const float4 o = *c;

@@ -821,7 +821,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const GemmEpilogue& e = p.epi;
     // acc scale: alpha times the operands' device scales (the FP8 path), if any
     float ealpha = e.alpha;
-    if constexpr (F8 == 1) ealpha *= (e.scale_a ? *e.scale_a : 1.f) * (e.scale_b ? *e.scale_b : 1.f);
+    if constexpr (F8 == 1 || (F8 == 0 && (KM == K_STORE || KM == K_STORE_F32 || KM == K_REDUCE_F32 || KM == K_PARTIAL)))
+      ealpha *= (e.scale_a ? *e.scale_a : 1.f) * (e.scale_b ? *e.scale_b : 1.f);
+    if constexpr (KM == K_DLOGITS) {
+      // the mean's gradient scale, counted by the first CTA's epilogue warps
+      // while its first tile is multiplied
+      if (blockIdx.x == 0 && e.base_out != nullptr) {
+        int* counts = reinterpret_cast<int*>(sturns);
+        int c = 0;
+        for (int i = ew * 32 + lane; i < p.M; i += 32 * EPI_WARPS) {
+          const int y = e.targets[i];
+          c += y >= 0 && y < e.vocab;
+        }
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (lane == 0) counts[ew] = c;
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
+        if (ew == 0 && lane == 0) {
+          c = 0;
+          for (int w = 0; w < EPI_WARPS; ++w) c += counts[w];
+          *e.base_out = c > 0 ? (e.dloss ? *e.dloss : 1.f) / (float)c : 0.f;
+        }
+      }
+    }
     constexpr bool f32out = KM == K_STORE_F32 || KM == K_REDUCE_F32 || KM == K_PARTIAL;
     constexpr bool has_aux = KM == K_DRELU2 || KM == K_AXPBY;
     constexpr int CW = f32out ? 32 : 64;  // columns per 128-byte staging row
@@ -871,9 +892,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int ytgt = -1;
       if constexpr (KM == K_DLOGITS) {
         if (m < p.M) {
-          ytgt = e.targets[m] - e.col0;
+          const int y = e.targets[m];
           row_lse = e.lse[m];
-          row_g = e.row_scale[m];
+          if (y >= 0 && y < e.vocab) {
+            row_g = e.dtok ? e.dtok[m] : 1.f;
+            ytgt = y - e.col0;
+          } else if (y != -1) {
+            set_error(p.err, GPT_EBIT_INPUT);
+          }
         }
       }
       if constexpr (KM == K_LSE) ytgt = m < p.M ? e.targets[m] : -1;

@@ -576,8 +576,9 @@ static GemmEpilogue epi(int mode, void* C, long long ldc, int beta = 0, void* C2
   e.rope = nullptr; e.rstd_q = e.rstd_k = nullptr; e.hv = nullptr; e.rv = nullptr;
   e.scale_a = e.scale_b = nullptr;
   e.aux_scale = 0.f;
-  e.lse = e.row_scale = nullptr;
-  e.col0 = 0;
+  e.lse = e.dtok = e.dloss = nullptr;
+  e.base_out = nullptr;
+  e.vocab = e.col0 = 0;
   e.counter = nullptr;
   e.T = e.H = e.qk_norm = 0; e.eps = 0.f;
   return e;

@@ -10,7 +10,10 @@
 // of size N x V is ever written; ce_combine_kernel joins a row's pairs.  The
 // backward pass walks the vocabulary in pieces: the logits of a piece once more,
 // turned into dz (bf16) in that GEMM's epilogue, then the two gradient products
-// on it; dx is summed over the pieces in fp32.  Three products of 2 N V d
+// on it; dx is summed over the pieces in fp32.  dz is rounded to bf16 without the
+// mean's factor dloss / count, which the products apply in fp32: where few rows have a target in
+// common, dz = -(1 - p) with p near 0 is then exact instead of off by the same
+// half step in every row.  Three products of 2 N V d
 // operations bound it.  fp32: the same pieces through plain FFMA products, with
 // fp32 logits of one piece at a time in the workspace.
 #pragma once
@@ -127,9 +130,9 @@ __global__ void __launch_bounds__(32 * G) ce_combine_kernel(const float2* __rest
   }
 }
 
-// Gradient scale of a row: dtok[i], or base = dloss / count (dloss null: 1), 0
-// for ignored rows.  Every block counts the targets itself (they are few and
-// in L2), so that no launch has to come first.
+// fp32: gradient scale of a row: dtok[i], or base = dloss / count (dloss null: 1),
+// 0 for ignored rows.  Every block counts the targets itself (they are in L2), so
+// that no launch has to come first.
 struct CeRowScale {
   const int32_t* targets;
   const float* dloss;
@@ -154,10 +157,11 @@ __device__ __forceinline__ float ce_row_scale(const CeRowScale& a, float base, i
   if (y < -1 || y >= a.V) set_error(a.err, GPT_EBIT_INPUT);
   return y >= 0 && y < a.V ? (a.dtok ? a.dtok[i] : base) : 0.f;
 }
-__global__ void __launch_bounds__(1024) ce_row_scale_kernel(const CeRowScale a, float* __restrict__ g) {
+// base alone, for more rows than the first CTA of the bf16 product counts on the side
+__global__ void __launch_bounds__(1024) ce_base_kernel(const CeRowScale a, float* __restrict__ base) {
   pdl_wait();
-  const float base = ce_scale_base(a);
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < a.N; i += gridDim.x * blockDim.x) g[i] = ce_row_scale(a, base, i);
+  const float b = ce_scale_base(a);
+  if (threadIdx.x == 0) *base = b;
 }
 
 // ---------------------------------------------------------------- fp32 pieces
@@ -313,15 +317,18 @@ __global__ void __launch_bounds__(CEP_WARPS * 32, 2) ce_product_kernel(const CeP
   }
 }
 
-// fp32 sum over the pieces -> dx (row pitch ld elements)
-__global__ void __launch_bounds__(256) ce_dx_kernel(const float* __restrict__ acc, int N, int d, bf16* __restrict__ dx,
-                                                    long long ld) {
+// fp32 sum over the pieces, times *base (null: 1) -> dx (row pitch ld elements)
+__global__ void __launch_bounds__(256) ce_dx_kernel(const float* __restrict__ acc, int N, int d,
+                                                    const float* __restrict__ base, bf16* __restrict__ dx, long long ld) {
   pdl_wait();
+  const float b = base ? *base : 1.f;
   const int c4 = d / 4;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < (long long)N * c4;
        i += (long long)gridDim.x * blockDim.x) {
     float v[4];
     load4(acc + i * 4, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] *= b;
     store4(dx + (i / c4) * ld + (i % c4) * 4, v);
   }
 }

@@ -248,7 +248,7 @@ static int ce_piece(int N, int V, int d, int dtype, int asked) {
 
 // Byte offsets of the operator's scratch inside the caller's workspace.
 struct CeWs {
-  size_t stats, ztgt, part, counter, rowg, dz, dx, splitk, total;
+  size_t stats, ztgt, part, counter, base, dz, dx, splitk, total;
   int piece, n_tiles;
   long long splitk_elems;
 };
@@ -266,10 +266,10 @@ static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) 
     w.counter = cv.take(4);
     if (!lp) w.dz = cv.take((size_t)N * w.piece * 4);
   } else {
-    if (lp) w.rowg = cv.take((size_t)N * 4);
+    w.base = cv.take(4);
     w.dz = cv.take((size_t)N * (lp ? 64 * cdiv(w.piece, 64) : w.piece) * (lp ? 2 : 4));
     if (lp) {
-      w.dx = cv.take((size_t)N * d * 4);
+      if (w.piece < V) w.dx = cv.take((size_t)N * d * 4);
       // split-K partials, for products of few output tiles
       w.splitk_elems = std::min<long long>(16LL * std::max<long long>(N, w.piece) * d, 32LL << 20);
       w.splitk = cv.take((size_t)w.splitk_elems * 4);
@@ -392,17 +392,19 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
   unsigned* err = nullptr;
   CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
   uint8_t* b = static_cast<uint8_t*>(workspace);
-  float* rowg = reinterpret_cast<float*>(b + p.rowg);
   const CeRowScale scale{targets, dloss, dtok, N, V, err};
-  if (lp) {
-    ++g_launches; launch_pdl(ce_row_scale_kernel, std::min(32, cdiv(N, 1024)), 1024, 0, st, scale, rowg);
+  // the mean's factor, applied by the products (bf16); per-token gradients go into dz
+  float* base = dtok ? nullptr : reinterpret_cast<float*>(b + p.base);
+  const bool count_aside = N > 4096;
+  if (lp && base && count_aside) {
+    ++g_launches; launch_pdl(ce_base_kernel, 1, 1024, 0, st, scale, base);
     LAUNCH_CHECK();
   }
   const GemmCtx g{lp, reinterpret_cast<float*>(b + p.splitk), p.splitk_elems, err, st, nullptr};
   const size_t es = dtype_size(dtype);
   void* dz = b + p.dz;
+  const bool one = p.piece >= V;  // dx needs no sum over pieces
   float* acc = lp ? reinterpret_cast<float*>(b + p.dx) : static_cast<float*>(dx);
-  const long long ldacc = lp ? d : lddx;
   for (int v0 = 0; v0 < V; v0 += p.piece) {
     const int width = std::min(p.piece, V - v0);
     const uint8_t* wp = static_cast<const uint8_t*>(w) + (size_t)v0 * ldw * es;
@@ -410,7 +412,8 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
     if (lp) {
       ldz = 64 * cdiv(width, 64);
       GemmEpilogue e = epi(EPI_DLOGITS, dz, ldz);
-      e.softcap = softcap; e.targets = targets; e.col0 = v0; e.lse = lse; e.row_scale = rowg;
+      e.softcap = softcap; e.targets = targets; e.vocab = V; e.col0 = v0; e.lse = lse; e.dtok = dtok; e.dloss = dloss;
+      if (v0 == 0 && !count_aside) e.base_out = base;
       TRY(gemm(g, N, width, d, op_k(x, ldx), op_k(wp, ldw), e));
     } else {
       float* z = static_cast<float*>(dz);
@@ -419,21 +422,26 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
       TRY(ce_products(ce_product(xf, ldx, 1, wf, ldw, 1, z, width, N, width, d, 0), CeProduct{},
                       CeGrad{lse, scale, v0, softcap}, st));
       CeProduct px = {}, pw = {};
-      if (dx) px = ce_product(z, width, 1, wf, ldw, 0, acc, ldacc, N, d, width, v0 > 0);
+      if (dx) px = ce_product(z, width, 1, wf, ldw, 0, acc, lddx, N, d, width, v0 > 0);
       if (dw) pw = ce_product(z, width, 0, xf, ldx, 0, static_cast<float*>(dw) + v0 * lddw, lddw, width, d, N, dw_beta);
       TRY(ce_products(px, pw, CeGrad{}, st));
       continue;
     }
-    if (dx) TRY(gemm(g, N, d, width, op_k(dz, ldz), op_mn(wp, ldw), epi(EPI_ACCUM_F32, acc, ldacc, v0 > 0), true));
+    if (dx) {
+      GemmEpilogue e = one ? epi(EPI_STORE, dx, lddx) : epi(EPI_ACCUM_F32, acc, d, v0 > 0);
+      if (one) e.scale_a = base;
+      TRY(gemm(g, N, d, width, op_k(dz, ldz), op_mn(wp, ldw), e, true));
+    }
     if (dw) {
       uint8_t* out = static_cast<uint8_t*>(dw) + (size_t)v0 * lddw * dtype_size(dw_dtype);
-      const GemmEpilogue e = dw_dtype == GPT_DTYPE_BF16 ? epi(EPI_STORE, out, lddw) : epi(EPI_ACCUM_F32, out, lddw, dw_beta);
+      GemmEpilogue e = dw_dtype == GPT_DTYPE_BF16 ? epi(EPI_STORE, out, lddw) : epi(EPI_ACCUM_F32, out, lddw, dw_beta);
+      e.scale_a = base;
       TRY(gemm(g, width, d, N, op_mn(dz, ldz), op_mn(x, ldx), e, true));
     }
   }
-  if (dx && lp) {
+  if (dx && lp && !one) {
     const int blocks = (int)std::min<long long>(((long long)N * d / 4 + 255) / 256, 8LL * device_sms());
-    ++g_launches; launch_pdl(ce_dx_kernel, blocks, 256, 0, st, (const float*)acc, N, d, (bf16*)dx, lddx);
+    ++g_launches; launch_pdl(ce_dx_kernel, blocks, 256, 0, st, (const float*)acc, N, d, (const float*)base, (bf16*)dx, lddx);
     LAUNCH_CHECK();
   }
   return GPT_OK;
