@@ -204,12 +204,19 @@ __global__ void __launch_bounds__(256) ce_piece_stats_kernel(const float* __rest
 // warps of a block take every eighth chunk of 16 k's each, through shared memory
 // of their own (no block barrier in the loop, the next chunk's loads in flight
 // meanwhile), 4 x 8 results per thread in packed pairs, and the partial tiles are
-// added in warp order.  FFMA bounds it at size; a small call is latency.
+// added in warp order.  Fewer tiles than SMs and a long K: K is also shared out
+// over blocks, whose tiles the last one to finish adds in share order.  A chunk
+// lies as [k][row ^ 8 (k / 4)], so that neither the writes of an operand that is
+// contiguous along k nor the reads conflict.  A small call is latency, a large one
+// the loads of the small tiles.
 struct CeProduct {
   const float* A; long long lda; int a_kmajor;
   const float* B; long long ldb; int b_kmajor;
   float* C; long long ldc;
   int M, N, K, beta, tiles;  // tiles = number of 32 x 32 tiles; 0: no product
+  int splits;                // shares of K
+  float* part;               // splits > 1: [tiles * splits][32 x 32]
+  unsigned* counter;         // splits > 1: finished shares per tile, zero at the start
 };
 // gradient epilogue (dz instead of z); lse null: none
 struct CeGrad {
@@ -217,66 +224,91 @@ struct CeGrad {
   CeRowScale scale;
   int col0;
   float softcap;
+  unsigned* zero;  // CEP_TILES counters to zero for the next launch (null: none)
 };
 constexpr int CEP_KC = 16, CEP_WARPS = 8;
+constexpr int CEP_TILES = 296;  // two blocks per SM: about as many as a split product makes
+constexpr int CEP_SLOTS = 2 * CEP_TILES;  // partial tiles
 
-// row r, columns k0 ... of an operand (zeros beyond it)
-__device__ __forceinline__ void ce_load_chunk(float (&v)[CEP_KC], const float* __restrict__ p, long long ld, int kmajor,
-                                              int r, int rows, int k0, int K) {
-  if (kmajor) {
-    const float* q = p + r * ld + k0;
-    if (r < rows && k0 + CEP_KC <= K && ((ld & 3) | (reinterpret_cast<uintptr_t>(p) & 15)) == 0) {
+// One lane's part of a 32 x 16 chunk (zeros beyond the operand): four times four
+// neighbours along the contiguous dimension.
+__device__ __forceinline__ void ce_load_chunk(float (&v)[4][4], const float* __restrict__ p, long long ld, int kmajor,
+                                              bool vec, int r0, int rows, int k0, int k1) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int k = 0; k < CEP_KC; k += 4) load4(q + k, *reinterpret_cast<float(*)[4]>(&v[k]));
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + (kmajor ? (lane >> 2) + 8 * i : (lane & 7) * 4), k = k0 + (kmajor ? (lane & 3) * 4 : (lane >> 3) + 4 * i);
+    const float* q = kmajor ? p + r * ld + k : p + k * ld + r;
+    if (vec && (kmajor ? r < rows && k + 4 <= k1 : k < k1 && r + 4 <= rows)) {
+      load4(q, v[i]);
     } else {
 #pragma unroll
-      for (int k = 0; k < CEP_KC; ++k) v[k] = r < rows && k0 + k < K ? q[k] : 0.f;
+      for (int j = 0; j < 4; ++j) v[i][j] = (kmajor ? r < rows && k + j < k1 : k < k1 && r + j < rows) ? q[j] : 0.f;
     }
-  } else {
+  }
+}
+__device__ __forceinline__ void ce_store_chunk(float (*s)[32], const float (&v)[4][4], int kmajor) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < CEP_KC; ++k) v[k] = r < rows && k0 + k < K ? p[(k0 + k) * ld + r] : 0.f;
+  for (int i = 0; i < 4; ++i) {
+    if (kmajor) {
+      const int kq = lane & 3, r = ((lane >> 2) + 8 * i) ^ (8 * kq);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[4 * kq + j][r] = v[i][j];
+    } else {
+      store4(&s[(lane >> 3) + 4 * i][((lane & 7) * 4) ^ (8 * i)], v[i]);
+    }
   }
 }
 
 // one or two products in one launch (dx and dW of a piece)
 __global__ void __launch_bounds__(CEP_WARPS * 32, 2) ce_product_kernel(const CeProduct p0, const CeProduct p1,
-                                                                    const CeGrad gr) {
+                                                                       const CeGrad gr) {
   pdl_wait();
   // per warp: its chunks of A and B; then its partial tile
   __shared__ __align__(16) float sh[CEP_WARPS][2][CEP_KC][32];
-  const bool second = (int)blockIdx.x >= p0.tiles;
+  __shared__ int last;
+  const int blocks0 = p0.tiles * p0.splits;
+  const bool second = (int)blockIdx.x >= blocks0;
   const CeProduct& p = second ? p1 : p0;
-  const int tile = blockIdx.x - (second ? p0.tiles : 0), nt = (p.N + 31) >> 5;
+  const int item = blockIdx.x - (second ? blocks0 : 0), tile = item / p.splits, nt = (p.N + 31) >> 5;
   const int m0 = tile / nt * 32, n0 = tile % nt * 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tm = (lane >> 2) * 4, tn = (lane & 3) * 8;  // this thread's 4 x 8 results
-  float (&as)[CEP_KC][32] = sh[warp][0];
-  float (&bs)[CEP_KC][32] = sh[warp][1];
+  float (*as)[32] = sh[warp][0];
+  float (*bs)[32] = sh[warp][1];
   constexpr int STEP = CEP_WARPS * CEP_KC;
+  const int share = ((p.K + p.splits * CEP_KC - 1) / (p.splits * CEP_KC)) * CEP_KC;
+  const int kb = item % p.splits * share, k1 = min(p.K, kb + share);
+  const bool veca = ((p.lda & 3) | (reinterpret_cast<uintptr_t>(p.A) & 15)) == 0;
+  const bool vecb = ((p.ldb & 3) | (reinterpret_cast<uintptr_t>(p.B) & 15)) == 0;
   float acc[4][8] = {};
-  float va[CEP_KC], vb[CEP_KC];
-  int k0 = warp * CEP_KC;
+  float va[4][4], vb[4][4];
+  int k0 = kb + warp * CEP_KC;
   const bool grad = gr.lse != nullptr && !second;
-  if (k0 < p.K) {
-    ce_load_chunk(va, p.A, p.lda, p.a_kmajor, m0 + lane, p.M, k0, p.K);
-    ce_load_chunk(vb, p.B, p.ldb, p.b_kmajor, n0 + lane, p.N, k0, p.K);
+  if (k0 < k1) {
+    ce_load_chunk(va, p.A, p.lda, p.a_kmajor, veca, m0, p.M, k0, k1);
+    ce_load_chunk(vb, p.B, p.ldb, p.b_kmajor, vecb, n0, p.N, k0, k1);
   }
+  if (gr.zero && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < CEP_TILES; i += CEP_WARPS * 32) gr.zero[i] = 0u;
   const float base = grad ? ce_scale_base(gr.scale) : 0.f;  // while the first chunk is on its way
-  for (; k0 < p.K; k0 += STEP) {
+  for (; k0 < k1; k0 += STEP) {
     __syncwarp();
-#pragma unroll
-    for (int k = 0; k < CEP_KC; ++k) { as[k][lane] = va[k]; bs[k][lane] = vb[k]; }
+    ce_store_chunk(as, va, p.a_kmajor);
+    ce_store_chunk(bs, vb, p.b_kmajor);
     __syncwarp();
-    if (k0 + STEP < p.K) {
-      ce_load_chunk(va, p.A, p.lda, p.a_kmajor, m0 + lane, p.M, k0 + STEP, p.K);
-      ce_load_chunk(vb, p.B, p.ldb, p.b_kmajor, n0 + lane, p.N, k0 + STEP, p.K);
+    if (k0 + STEP < k1) {
+      ce_load_chunk(va, p.A, p.lda, p.a_kmajor, veca, m0, p.M, k0 + STEP, k1);
+      ce_load_chunk(vb, p.B, p.ldb, p.b_kmajor, vecb, n0, p.N, k0 + STEP, k1);
     }
 #pragma unroll 4
     for (int k = 0; k < CEP_KC; ++k) {
+      const int x = (k >> 2) * 8;
       float a[4], b[8];
-      load4(&as[k][tm], a);
-      load4(&bs[k][tn], *reinterpret_cast<float(*)[4]>(&b[0]));
-      load4(&bs[k][tn + 4], *reinterpret_cast<float(*)[4]>(&b[4]));
+      load4(&as[k][tm ^ x], a);
+      load4(&bs[k][tn ^ x], *reinterpret_cast<float(*)[4]>(&b[0]));
+      load4(&bs[k][(tn + 4) ^ x], *reinterpret_cast<float(*)[4]>(&b[4]));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -295,9 +327,24 @@ __global__ void __launch_bounds__(CEP_WARPS * 32, 2) ce_product_kernel(const CeP
 #pragma unroll
   for (int w = 0; w < CEP_WARPS; ++w) {
     float v[4];
-    load4(&sh[w][0][0][0] + (threadIdx.x >> 3) * 32 + nc, v);
+    load4(&sh[w][0][0][0] + threadIdx.x * 4, v);
 #pragma unroll
     for (int j = 0; j < 4; ++j) r[j] += v[j];
+  }
+  if (p.splits > 1) {
+    float4* part = reinterpret_cast<float4*>(p.part) + (long long)tile * p.splits * 256 + threadIdx.x;
+    part[item % p.splits * 256] = make_float4(r[0], r[1], r[2], r[3]);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(p.counter + tile, 1u) == (unsigned)p.splits - 1;
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    r[0] = r[1] = r[2] = r[3] = 0.f;
+    for (int s = 0; s < p.splits; ++s) {
+      const float4 v = __ldcg(part + s * 256);
+      r[0] += v.x; r[1] += v.y; r[2] += v.z; r[3] += v.w;
+    }
   }
   if (m >= p.M) return;
   const float l = grad ? gr.lse[m] : 0.f, g = grad ? ce_row_scale(gr.scale, base, m) : 0.f;

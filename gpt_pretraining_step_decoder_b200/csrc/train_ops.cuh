@@ -273,6 +273,9 @@ static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) 
       // split-K partials, for products of few output tiles
       w.splitk_elems = std::min<long long>(16LL * std::max<long long>(N, w.piece) * d, 32LL << 20);
       w.splitk = cv.take((size_t)w.splitk_elems * 4);
+    } else {
+      w.splitk = cv.take((size_t)CEP_SLOTS * 1024 * 4);
+      w.counter = cv.take((size_t)CEP_TILES * 4);
     }
   }
   w.total = cv.take(0);
@@ -281,14 +284,29 @@ static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) 
 
 static CeProduct ce_product(const float* A, long long lda, int a_kmajor, const float* B, long long ldb, int b_kmajor,
                             float* C, long long ldc, int M, int N, int K, int beta) {
-  return CeProduct{A, lda, a_kmajor, B, ldb, b_kmajor, C, ldc, M, N, K, beta, cdiv(M, 32) * cdiv(N, 32)};
+  return CeProduct{A, lda, a_kmajor, B, ldb, b_kmajor, C, ldc, M, N, K, beta, cdiv(M, 32) * cdiv(N, 32), 1, nullptr, nullptr};
+}
+// Shares of K for products of fewer tiles than SMs: about two blocks per SM,
+// at least one chunk for every warp of a block.  `part` has room for CEP_SLOTS
+// partial tiles, `counter` for CEP_TILES tiles.
+static void ce_split(CeProduct& p0, CeProduct& p1, float* part, unsigned* counter) {
+  for (CeProduct* p : {&p0, &p1}) {
+    if (p->tiles < 1 || p->tiles > CEP_TILES / 2) continue;
+    p->splits = std::max(1, std::min(CEP_TILES / p->tiles, cdiv(p->K, CEP_WARPS * CEP_KC)));
+    p->part = part;
+    p->counter = counter;
+    part += (size_t)p->tiles * p->splits * 1024;
+    counter += p->tiles;
+  }
 }
 static int ce_products(const CeProduct& p0, const CeProduct& p1, const CeGrad& gr, cudaStream_t st) {
   ++g_launches;
-  launch_pdl(ce_product_kernel, p0.tiles + p1.tiles, CEP_WARPS * 32, 0, st, p0, p1, gr);
+  launch_pdl(ce_product_kernel, p0.tiles * p0.splits + p1.tiles * p1.splits, CEP_WARPS * 32, 0, st, p0, p1, gr);
   LAUNCH_CHECK();
   return GPT_OK;
 }
+
+static const CeProduct ce_no_product = ce_product(nullptr, 0, 0, nullptr, 0, 0, nullptr, 0, 0, 0, 0, 0);
 
 static int ce_check(const char* fn, const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V,
                     int d, const int32_t* targets, float softcap) {
@@ -346,7 +364,7 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
       const int width = std::min(p.piece, V - v0);
       TRY(ce_products(ce_product(static_cast<const float*>(x), ldx, 1, static_cast<const float*>(w) + v0 * ldw, ldw, 1, z,
                                  width, N, width, d, 0),
-                      CeProduct{}, CeGrad{}, st));
+                      ce_no_product, CeGrad{}, st));
       ++g_launches; launch_pdl(ce_piece_stats_kernel, N, 256, 0, st, (const float*)z, width, v0, v0 == 0 ? 1 : 0, softcap,
                                targets, N, stats, ztgt, counter);
       LAUNCH_CHECK();
@@ -393,6 +411,7 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
   CUDA_TRY(cudaGetSymbolAddress((void**)&err, g_ngram_err));
   uint8_t* b = static_cast<uint8_t*>(workspace);
   const CeRowScale scale{targets, dloss, dtok, N, V, err};
+  unsigned* counter = reinterpret_cast<unsigned*>(b + p.counter);
   // the mean's factor, applied by the products (bf16); per-token gradients go into dz
   float* base = dtok ? nullptr : reinterpret_cast<float*>(b + p.base);
   const bool count_aside = N > 4096;
@@ -420,10 +439,11 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
       const float* xf = static_cast<const float*>(x);
       const float* wf = reinterpret_cast<const float*>(wp);
       TRY(ce_products(ce_product(xf, ldx, 1, wf, ldw, 1, z, width, N, width, d, 0), CeProduct{},
-                      CeGrad{lse, scale, v0, softcap}, st));
-      CeProduct px = {}, pw = {};
+                      CeGrad{lse, scale, v0, softcap, counter}, st));
+      CeProduct px = ce_no_product, pw = ce_no_product;
       if (dx) px = ce_product(z, width, 1, wf, ldw, 0, acc, lddx, N, d, width, v0 > 0);
       if (dw) pw = ce_product(z, width, 0, xf, ldx, 0, static_cast<float*>(dw) + v0 * lddw, lddw, width, d, N, dw_beta);
+      ce_split(px, pw, reinterpret_cast<float*>(b + p.splitk), counter);
       TRY(ce_products(px, pw, CeGrad{}, st));
       continue;
     }
