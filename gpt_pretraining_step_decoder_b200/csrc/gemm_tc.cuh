@@ -238,6 +238,9 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
                    smem_u32(bar))
                : "memory");
 }
+__device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
                                             int z) {
   asm volatile(
@@ -599,7 +602,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmAux,
                    const __grid_constant__ Params p) {
-  pdl_wait();     // the previous kernel in the stream has completed (programmatic launch)
   using C = Cfg<BN, KmHeavy<KM>::value, CG, F8 == 2>;
   static_assert(CG == 1 || CG == 2, "one CTA or a CTA pair per tile");
   constexpr int KE = F8 ? 128 : BK;  // operand elements per 128-byte k-block row
@@ -622,10 +624,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   static_assert((2 * C::STAGES + 4 + EPI_WARPS * C::NAUX) * 8 + 8 <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if constexpr (KM == K_LSE)
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.epi.counter = 0u;
-  if constexpr (KM == K_QKV)
-    if (threadIdx.x < 64 && p.epi.rope != nullptr) sturns[threadIdx.x] = p.epi.rope[threadIdx.x];
   const int per_product = p.m_tiles * p.n_tiles * p.splits;
   const int tiles = B3 ? per_product * p.batch : per_product;
   // CTA pair: rank 0 issues the MMAs; tile t goes to pair blockIdx.x / CG
@@ -636,6 +634,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const int t_first = RUNS ? 0 : unit, t_step = RUNS ? 1 : n_units;
   const int t_end = RUNS ? run_walk(unit, n_units, p) : tiles;
 
+  if (threadIdx.x == 32) {
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+    if constexpr (F8 == 2) { prefetch_tmap(&p.tm_sfa); prefetch_tmap(&p.tm_sfb); }
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     // tempty: one arrival per epilogue warp (of both CTAs of a pair)
@@ -666,6 +669,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if constexpr (CG == 2) cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  // so far only shared and tensor memory: set up while the kernel before this
+  // one in the stream still finishes
+  pdl_wait();
+  if constexpr (KM == K_LSE)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.epi.counter = 0u;
+  if constexpr (KM == K_QKV) {
+    if (threadIdx.x < 64 && p.epi.rope != nullptr) sturns[threadIdx.x] = p.epi.rope[threadIdx.x];
+    __syncthreads();
+  }
 
   if (warp == 0) {
     if (lane == 0) {
