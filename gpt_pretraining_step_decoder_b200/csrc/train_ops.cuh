@@ -103,31 +103,38 @@ extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long
   return quantize_launch((const float*)x, a, st);
 }
 
-// Tile shape and K split of a block-scaled product: pairs of SMs (256-row
-// tiles) where there is more than one block of 128 rows, and the width (256 or
-// 128 columns) and split with the least estimated time, in SM cycles: whole
-// waves of tiles, each k-block the longer of its MMAs and of its operands' way
-// from L2 (about 64 bytes a cycle and SM), plus the tile's start and epilogue;
-// a split adds its second launch and the partials' way through L2.  K is split in
-// whole scale atoms (4 k-blocks).
+// Tile shape (256 or 128 columns, one SM or a pair) and K split of a
+// block-scaled product: the form with the least estimated time,
+//   fixed + waves * (k-blocks * c + e) + split,
+// in microseconds measured on B200 (launch to launch, over 23 shapes from 1 x 8 x
+// 16 to 8192 x 2048 x 16384; the choice is within 8% of the best form on each).  A
+// pair costs 1.2 us more to start and, with its one accumulator, more between
+// tiles, but moves fewer bytes per product once all SMs pull on L2: short
+// products run on one SM per tile (4096 x 4096 x 128: 9.4 us against 13.7 on
+// pairs, 200 x 768 x 768: 5.4 against 6.9), long ones on pairs (8192 x 2048 x 16384:
+// 206 against 245).  A split adds its second launch and the partials' way
+// through L2; K is split in whole scale atoms (4 k-blocks).
 struct F8bPlan { int bn, cg, splits; };
 static F8bPlan f8b_plan(int M, int N, int K) {
-  const int cg = M > 128 && gemm_pairs_enabled() ? 2 : 1;
-  const int quads = cdiv(K, 512), units = device_sms() / cg;
-  F8bPlan best{128, cg, 1};
+  const int quads = cdiv(K, 512), kb = cdiv(K, 128), sms = device_sms();
+  F8bPlan best{128, 1, 1};
   double best_t = 1e300;
-  for (int bn : {256, 128}) {
-    if (bn == 256 && N <= 128) continue;
-    const double kb_cycles = std::max(2.0 * bn, (128 + bn / cg) * 128 / 64.0);
-    const long long tiles = (long long)cdiv(M, 128 * cg) * cdiv(N, bn);
-    for (int s = 1; s <= (N % 4 == 0 && tiles < units ? std::min(32, quads) : 1); ++s) {
-      const int share = cdiv(quads, s);
-      if (cdiv(quads, share) != s) continue;  // the same shares as a smaller split
-      const double waves = (double)((tiles * s + units - 1) / units);
-      const double t = waves * (share * 4 * kb_cycles + 1500.0) + (s > 1 ? 6000.0 + (double)s * M * N * 8 / 5000.0 : 0.0);
-      if (t < best_t) { best = F8bPlan{bn, cg, s}; best_t = t; }
+  for (int cg = 1; cg <= (M > 128 && gemm_pairs_enabled() ? 2 : 1); ++cg)
+    for (int bn : {128, 256}) {
+      if (bn == 256 && N <= 128) continue;
+      const long long tiles = (long long)cdiv(M, 128 * cg) * cdiv(N, bn), units = sms / cg;
+      for (int s = 1; s <= (N % 4 == 0 && tiles < units ? std::min(32, quads) : 1); ++s) {
+        const int share = cdiv(quads, s);
+        if (cdiv(quads, share) != s) continue;  // the same shares as a smaller split
+        const double busy = std::min(1.0, (double)(tiles * s) / units);  // share of the SMs that load
+        const double c = cg == 2 ? (bn == 256 ? 0.355 : 0.28) : (bn == 256 ? 0.31 + 0.16 * busy : 0.30);
+        const double e = cg == 2 ? (bn == 256 ? 1.75 : 1.3) : (bn == 256 ? 1.17 : 0.65);
+        const double waves = (double)((tiles * s + units - 1) / units);
+        const double t = (cg == 2 ? 4.4 : 3.2) + waves * (std::min(kb, 4 * share) * c + e) +
+                         (s > 1 ? 1.5 + (double)s * M * N * 8e-7 : 0.0);
+        if (t < best_t) { best = F8bPlan{bn, cg, s}; best_t = t; }
+      }
     }
-  }
   return best;
 }
 
