@@ -267,10 +267,14 @@ static int make_tmap3(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t 
   return make_tmap_gen(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, ptr, dims, str, box);
 }
 
-// Column tiles per run of the cross entropy's statistics: 4 where that leaves
-// the units many runs each (their last wave is then a small part), else 1.
+// Column tiles per run of the cross entropy's statistics: one run for each unit
+// where there is a single row block (as even as tiles go, and the fewest pairs to
+// join), else 4 where that leaves the units many runs each (their last wave is then
+// a small part), else 1.
 static int lse_run(int M, int N, int BN, int cg) {
-  return (long long)cdiv(M, 128 * cg) * cdiv(N, BN) >= 128LL * (device_sms() / cg) ? 4 : 1;
+  const int m = cdiv(M, 128 * cg), n = cdiv(N, BN), units = device_sms() / cg;
+  if (m <= 1) return std::max(1, cdiv(n, units));
+  return (long long)m * n >= 128LL * units ? 4 : 1;
 }
 
 template <int BN, int CG = 1>
@@ -517,15 +521,41 @@ struct GemmCtx {
   unsigned* err;
   cudaStream_t st;
   Prof* prof;
+  bool any_tile = false;  // tile shape and split by tile_plan
 };
 
-// The cross entropy's products of one block of rows run on one SM per tile: a
-// pair's other half would idle (33 x 50304 x 768: 24.4 us on pairs, 19.3 on one SM).
-static bool ce_half_pair(int M) { return M <= 128; }
+// Tile shape (256 or 128 columns, one SM or a pair) and K split of a bf16 product
+// with `any_tile` (the standalone cross entropy's, of any size): the form with
+// the least estimated time, fixed + waves * (k-blocks * c + e) + split, in
+// microseconds measured on B200.  A pair starts 1.2 us later and moves fewer bytes per
+// product once all SMs pull on L2 (33 x 50304 x 768: 24.4 us on pairs, 19.3 on one SM;
+// 32768 x 50304 x 768: 1618 and 1699); a split adds its second launch (on the
+// device and the host) and the partials' way through L2.  split_elems: room for fp32 partials (0: no split).
+struct TilePlan { int bn, cg, splits; };
+static TilePlan tile_plan(int M, int N, int K, long long split_elems) {
+  const int kb = cdiv(K, 64), sms = device_sms();
+  TilePlan best{128, 1, 1};
+  double best_t = 1e300;
+  for (int cg = 1; cg <= (M > 128 && N >= 256 && gemm_pairs_enabled() ? 2 : 1); ++cg)
+    for (int bn : {256, 128}) {
+      if (bn == 256 ? N < 256 : cg == 2) continue;
+      const long long tiles = (long long)cdiv(M, 128 * cg) * cdiv(N, bn), units = sms / cg;
+      const long long room = N % 4 == 0 && tiles < units ? split_elems / std::max(1LL, (long long)M * N) : 1;
+      for (int s = 1; s <= 16 && (s == 1 || (s <= room && kb / s >= 4)); ++s) {
+        const double busy = std::min(1.0, (double)(tiles * s) / units);  // share of the SMs that load
+        const double c = cg == 2 ? 0.34 : (bn == 256 ? 0.31 + 0.16 * busy : 0.30);
+        const double t = (cg == 2 ? 4.4 : 3.2) +
+                         (double)cdiv_ll(tiles * s, units) * (cdiv(kb, s) * c + (bn == 256 ? 0.5 : 0.35)) +
+                         (s > 1 ? 3.0 + (double)s * M * N * 8e-7 : 0.0);
+        if (t < best_t) { best = TilePlan{bn, cg, s}; best_t = t; }
+      }
+    }
+  return best;
+}
 // Pairs of statistics per row that an EPI_LSE product leaves (two per run of tiles).
-static int lse_pairs(int M, int N) {
-  const int cg = N >= 256 && gemm_pairs_enabled() && !ce_half_pair(M) ? 2 : 1, bn = N >= 256 ? 256 : 128;
-  return 2 * cdiv(cdiv(N, bn), lse_run(M, N, bn, cg));
+static int lse_pairs(int M, int N, int K) {
+  const TilePlan t = tile_plan(M, N, K, 0);
+  return 2 * cdiv(cdiv(N, t.bn), lse_run(M, N, t.bn, t.cg));
 }
 
 static int gemm(const GemmCtx& g, int M, int N, int K, GemmOperand A, GemmOperand B, GemmEpilogue e,
@@ -550,8 +580,13 @@ static int gemm(const GemmCtx& g, int M, int N, int K, GemmOperand A, GemmOperan
   // statistics and the ReLU^2 backward's activation stream), which measured
   // faster on one-SM tiles (B200: LM-head logits 2.55 vs 2.79 ms, ReLU^2
   // backward 2.04 vs 2.17 ms per GPT-2-small step)
-  const bool half_pair = ce_half_pair(M) && (e.mode == EPI_LSE || e.mode == EPI_DLOGITS);
-  if (N >= 256 && gemm_pairs_enabled() && e.mode != EPI_LOGITS && e.mode != EPI_DRELU2 && !half_pair)
+  if (g.any_tile) {
+    const TilePlan t = tile_plan(M, N, K, split_ok ? g.splitk_elems : 0);
+    if (t.cg == 2) return gemm_tc_launch<256, 2>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
+    if (t.bn == 256) return gemm_tc_launch<256>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
+    return gemm_tc_launch<128>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
+  }
+  if (N >= 256 && gemm_pairs_enabled() && e.mode != EPI_LOGITS && e.mode != EPI_DRELU2)
     return gemm_tc_launch<256, 2>(M, N, K, A, B, e, splits_for(256, 2), g.splitk, g.err, g.st);
   // one-CTA tiles: 256 wide (128 below 256 columns); fp32 outputs may take 192
   // when that fills the last wave of SMs better (N = 768: 4 x 192 instead of 3 x 256)

@@ -265,9 +265,8 @@ static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) 
   const bool lp = dtype == GPT_DTYPE_BF16;
   w.piece = ce_piece(N, V, d, dtype, asked);
   if (!backward) {
-    w.n_tiles = lp ? lse_pairs(N, V) : 1;
-    // room for either tile shape, whichever is set when the call comes
-    w.stats = cv.take((size_t)(lp ? 2 * cdiv(V, V >= 256 ? 256 : 128) : 1) * N * 8);
+    w.n_tiles = lp ? lse_pairs(N, V, d) : 1;
+    w.stats = cv.take((size_t)w.n_tiles * N * 8);
     w.ztgt = cv.take((size_t)N * 4);
     w.part = cv.take((size_t)cdiv(N, 32) * 16);
     w.counter = cv.take(4);
@@ -360,7 +359,7 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
   float* ztgt = reinterpret_cast<float*>(b + p.ztgt);
   double2* part = reinterpret_cast<double2*>(b + p.part);
   unsigned* counter = reinterpret_cast<unsigned*>(b + p.counter);
-  const GemmCtx g{dtype == GPT_DTYPE_BF16, nullptr, 0, err, st, nullptr};
+  const GemmCtx g{dtype == GPT_DTYPE_BF16, nullptr, 0, err, st, nullptr, true};
   if (g.bf16) {
     GemmEpilogue e = epi(EPI_LSE, nullptr, V);
     e.softcap = softcap; e.stats = stats; e.targets = targets; e.ztgt = ztgt; e.counter = counter;
@@ -426,7 +425,7 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
     ++g_launches; launch_pdl(ce_base_kernel, 1, 1024, 0, st, scale, base);
     LAUNCH_CHECK();
   }
-  const GemmCtx g{lp, reinterpret_cast<float*>(b + p.splitk), p.splitk_elems, err, st, nullptr};
+  const GemmCtx g{lp, reinterpret_cast<float*>(b + p.splitk), p.splitk_elems, err, st, nullptr, true};
   const size_t es = dtype_size(dtype);
   void* dz = b + p.dz;
   const bool one = p.piece >= V;  // dx needs no sum over pieces

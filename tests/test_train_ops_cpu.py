@@ -130,7 +130,9 @@ def test_ce_backward_refusals(bad):
 
 def test_ce_workspace():
     assert ce_forward(loss=None) == g.GPT_ERR_ARG
-    assert g.linear_ce_workspace_bytes(0, 100, 64, g.DTYPE_BF16, 1) >= 0
+    for dtype in (g.DTYPE_BF16, g.DTYPE_F32):
+        for back in (0, 1):
+            assert g.linear_ce_workspace_bytes(0, 100, 64, dtype, back) >= 0
     for call, back in ((ce_forward, 0), (ce_backward, 1)):
         need = g.linear_ce_workspace_bytes(10, 100, 64, g.DTYPE_BF16, back)
         assert need > 0 and call(ws_bytes=need - 1) == g.GPT_ERR_WORKSPACE
