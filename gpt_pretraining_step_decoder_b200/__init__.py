@@ -359,7 +359,7 @@ def fp8_block_scales(scales, rows, cols):
     """The stored scales of a [rows, cols] matrix as a plain uint8 tensor
     [rows, ceil(cols / 128)] of exponent bytes (a scale is 2^(byte - 127))."""
     ra, ga, groups = -(-rows // 128), -(-cols // 512), -(-cols // 128)
-    return scales.view(ga, ra, 32, 4, 4).permute(1, 3, 2, 0, 4).reshape(ra * 128, ga * 4)[:rows, :groups]
+    return scales.reshape(-1)[:ra * ga * 512].view(ga, ra, 32, 4, 4).permute(1, 3, 2, 0, 4).reshape(ra * 128, ga * 4)[:rows, :groups]
 
 
 def gptx_gemm_fp8_block_workspace_bytes(M, N, K):

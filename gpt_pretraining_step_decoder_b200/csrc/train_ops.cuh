@@ -45,14 +45,43 @@ struct DeviceScope {
   TRY(scope_.enter(fn, p))
 #define CHECK_PTR(fn, p) TRY(scope_.check(fn, #p, p))
 
+// A strided block of rows in memory, for the checks that a call's outputs do not
+// overlap what it reads or writes elsewhere.
+struct Span {
+  const char* name;
+  const void* p;
+  long long rows;
+  unsigned long long row_bytes, pitch;
+};
+static bool spans_overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || !a.row_bytes || !b.row_bytes) return false;
+  const unsigned long long a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const unsigned long long a1 = a0 + (a.rows - 1) * a.pitch + a.row_bytes, b1 = b0 + (b.rows - 1) * b.pitch + b.row_bytes;
+  if (a1 <= b0 || b1 <= a0) return false;
+  // columns side by side in rows of one pitch do not touch
+  if (a.pitch == b.pitch && a.pitch > 0) {
+    const unsigned long long shift = b0 >= a0 ? (b0 - a0) % a.pitch : (a.pitch - (a0 - b0) % a.pitch) % a.pitch;
+    if (shift >= a.row_bytes && shift + b.row_bytes <= a.pitch) return false;
+  }
+  return true;
+}
+// outputs first: each against everything behind it
+static int check_spans(const char* fn, const Span* s, int outputs, int n) {
+  for (int i = 0; i < outputs; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (spans_overlap(s[i], s[j])) return fail(GPT_ERR_ARG, "%s: %s overlaps %s", fn, s[i].name, s[j].name);
+  return GPT_OK;
+}
+
 static bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 static size_t dtype_size(int dtype) { return dtype == GPT_DTYPE_BF16 ? 2 : 4; }
 
 // ======================================================================== block-scaled FP8
+constexpr long long MAX_ROWS = 1LL << 30;  // rows or columns: tile coordinates stay in 32 bits
 static long long scale_atoms(long long rows, long long cols) { return cdiv_ll(rows, 128) * cdiv_ll(cols, 512); }
 
 extern "C" int fp8_block_scale_bytes(long long rows, long long cols, size_t* bytes) {
-  if (!bytes || rows < 1 || cols < 1 || rows > (1LL << 31) || cols > (1LL << 31))
+  if (!bytes || rows < 1 || cols < 1 || rows > MAX_ROWS || cols > MAX_ROWS)
     return fail(GPT_ERR_ARG, "fp8_block_scale_bytes: bad argument");
   *bytes = (size_t)scale_atoms(rows, cols) * 512;
   return GPT_OK;
@@ -82,7 +111,7 @@ extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long
                                   uint8_t* q, long long ldq, uint8_t* scales, uint8_t* qt, long long ldqt,
                                   uint8_t* scales_t, void* stream) {
   const char* fn = "fp8_block_quantize";
-  if (!x || rows < 0 || cols < 0 || rows > (1LL << 31) || cols > (1LL << 31) || ldx < cols || (!q && !qt))
+  if (!x || rows < 0 || cols < 0 || rows > MAX_ROWS || cols > MAX_ROWS || ldx < cols || (!q && !qt))
     return fail(GPT_ERR_ARG, "%s: bad argument", fn);
   if (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16) return fail(GPT_ERR_ARG, "%s: bad dtype", fn);
   if ((q && (!scales || ldq < cols || ldq % 16 || misaligned(q, 16) || misaligned(scales, 16))) ||
@@ -92,6 +121,12 @@ extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long
   if (misaligned(x, dtype_size(dtype))) return fail(GPT_ERR_ARG, "%s: x is not aligned to its elements", fn);
   const long long tiles = cdiv_ll(rows, 128) * cdiv_ll(cols, 128);
   if (tiles == 0) return GPT_OK;
+  const unsigned long long sb = scale_atoms(rows, cols) * 512, sbt = scale_atoms(cols, rows) * 512;
+  const Span spans[] = {{"q", q, rows, (unsigned long long)cols, (unsigned long long)ldq}, {"scales", q ? scales : nullptr, 1, sb, 0},
+                        {"qt", qt, cols, (unsigned long long)rows, (unsigned long long)ldqt},
+                        {"scales_t", qt ? scales_t : nullptr, 1, sbt, 0},
+                        {"x", x, rows, cols * dtype_size(dtype), ldx * dtype_size(dtype)}};
+  TRY(check_spans(fn, spans, 4, 5));
   if (tiles > 0x7fffffffLL) return fail(GPT_ERR_ARG, "%s: too many elements", fn);
   cudaStream_t st = (cudaStream_t)stream;
   ON_DEVICE_OF(fn, x);
@@ -187,7 +222,8 @@ static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda,
 }
 
 extern "C" int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes) {
-  if (!bytes || M < 1 || N < 1 || K < 1) return fail(GPT_ERR_ARG, "gptx_gemm_fp8_block_workspace_bytes: bad argument");
+  if (!bytes || M < 1 || N < 1 || K < 1 || M > MAX_ROWS || N > MAX_ROWS || K > MAX_ROWS)
+    return fail(GPT_ERR_ARG, "gptx_gemm_fp8_block_workspace_bytes: bad argument");
   const F8bPlan pl = f8b_plan(M, N, K);
   *bytes = pl.splits > 1 ? (size_t)pl.splits * M * N * 4 : 0;
   return GPT_OK;
@@ -197,7 +233,8 @@ extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long l
                                    const uint8_t* B, long long ldb, const uint8_t* scales_b, int out_dtype, void* C,
                                    long long ldc, int beta, void* workspace, size_t ws_bytes, void* stream) {
   const char* fn = "gptx_gemm_fp8_block";
-  if (M < 1 || N < 1 || K < 1 || !A || !B || !C || !scales_a || !scales_b || ldc < N || lda < K || ldb < K)
+  if (M < 1 || N < 1 || K < 1 || M > MAX_ROWS || N > MAX_ROWS || K > MAX_ROWS || !A || !B || !C || !scales_a ||
+      !scales_b || ldc < N || lda < K || ldb < K)
     return fail(GPT_ERR_ARG, "%s: bad argument", fn);
   if (out_dtype != GPT_DTYPE_F32 && out_dtype != GPT_DTYPE_BF16) return fail(GPT_ERR_ARG, "%s: bad out_dtype", fn);
   if (beta && out_dtype != GPT_DTYPE_F32) return fail(GPT_ERR_ARG, "%s: beta needs an fp32 output", fn);
@@ -210,6 +247,11 @@ extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long l
   if (need && (!workspace || ws_bytes < need))
     return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, need);
   if (need && misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
+  const Span spans[] = {{"C", C, M, N * dtype_size(out_dtype), ldc * dtype_size(out_dtype)},
+                        {"the workspace", need ? workspace : nullptr, 1, need, 0},
+                        {"A", A, M, (unsigned long long)K, (unsigned long long)lda}, {"B", B, N, (unsigned long long)K, (unsigned long long)ldb},
+                        {"scales_a", scales_a, 1, scale_atoms(M, K) * 512ull, 0}, {"scales_b", scales_b, 1, scale_atoms(N, K) * 512ull, 0}};
+  TRY(check_spans(fn, spans, 2, 6));
   ON_DEVICE_OF(fn, A);
   CHECK_PTR(fn, B); CHECK_PTR(fn, C); CHECK_PTR(fn, scales_a); CHECK_PTR(fn, scales_b);
   if (need) CHECK_PTR(fn, workspace);
@@ -233,7 +275,7 @@ extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long l
 // fp32 dx each, fewer cost memory.
 static int ce_piece(int N, int V, int d, int dtype, int asked) {
   const int tiles = cdiv(V, 256);
-  if (asked > 0) return std::min(V, 64 * cdiv(asked, 64));
+  if (asked > 0) return std::min(V, 64 * cdiv(std::min(asked, V), 64));
   const long long budget = 512LL << 20, col_bytes = std::max(N, 1) * (long long)(dtype == GPT_DTYPE_BF16 ? 2 : 4) * 256;
   const int most = (int)std::max<long long>(1, std::min<long long>(tiles, budget / col_bytes));
   if (most >= tiles || dtype != GPT_DTYPE_BF16) return std::min(V, most * 256);
@@ -316,7 +358,7 @@ static const CeProduct ce_no_product = ce_product(nullptr, 0, 0, nullptr, 0, 0, 
 
 static int ce_check(const char* fn, const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V,
                     int d, const int32_t* targets, float softcap) {
-  if (N < 0 || V < 1 || d < 1 || !w || (N > 0 && (!x || !targets)) || ldx < d || ldw < d || !(softcap >= 0.f) ||
+  if (N < 0 || V < 1 || d < 1 || N > MAX_ROWS || V > MAX_ROWS || d > MAX_ROWS || !w || (N > 0 && (!x || !targets)) || ldx < d || ldw < d || !(softcap >= 0.f) ||
       std::isinf(softcap))
     return fail(GPT_ERR_ARG, "%s: bad argument", fn);
   if (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16) return fail(GPT_ERR_ARG, "%s: bad dtype", fn);
@@ -329,7 +371,7 @@ static int ce_check(const char* fn, const void* x, long long ldx, const void* w,
 }
 
 extern "C" int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int vocab_piece, size_t* bytes) {
-  if (!bytes || N < 0 || V < 1 || d < 1 || vocab_piece < 0 || (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16))
+  if (!bytes || N < 0 || V < 1 || d < 1 || N > MAX_ROWS || V > MAX_ROWS || d > MAX_ROWS || vocab_piece < 0 || (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16))
     return fail(GPT_ERR_ARG, "linear_ce_workspace_bytes: bad argument");
   *bytes = ce_ws_plan(N, V, d, dtype, backward != 0, vocab_piece).total;
   return GPT_OK;
@@ -345,6 +387,11 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
   const CeWs p = ce_ws_plan(N, V, d, dtype, 0, vocab_piece);
   if (!workspace || ws_bytes < p.total) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, p.total);
   if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
+  const size_t fes = dtype_size(dtype);
+  const Span spans[] = {{"loss", loss, 1, 4, 0}, {"tok_loss", tok_loss, 1, N * 4ull, 0}, {"lse", lse, 1, N * 4ull, 0},
+                        {"the workspace", workspace, 1, p.total, 0}, {"x", x, N, d * fes, ldx * fes}, {"w", w, V, d * fes, ldw * fes},
+                        {"targets", targets, 1, N * 4ull, 0}};
+  TRY(check_spans(fn, spans, 4, 7));
   cudaStream_t st = (cudaStream_t)stream;
   ON_DEVICE_OF(fn, workspace);
   CHECK_PTR(fn, x); CHECK_PTR(fn, w); CHECK_PTR(fn, targets); CHECK_PTR(fn, loss); CHECK_PTR(fn, tok_loss); CHECK_PTR(fn, lse);
@@ -404,6 +451,11 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
   const CeWs p = ce_ws_plan(N, V, d, dtype, 1, vocab_piece);
   if (!workspace || ws_bytes < p.total) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, p.total);
   if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
+  const size_t bes = dtype_size(dtype), wes = dtype_size(dw_dtype);
+  const Span spans[] = {{"dx", dx, N, d * bes, lddx * bes}, {"dw", dw, V, d * wes, lddw * wes}, {"the workspace", workspace, 1, p.total, 0},
+                        {"x", x, N, d * bes, ldx * bes}, {"w", w, V, d * bes, ldw * bes}, {"targets", targets, 1, N * 4ull, 0},
+                        {"lse", lse, 1, N * 4ull, 0}, {"dtok", dtok, 1, N * 4ull, 0}, {"dloss", dloss, 1, 4, 0}};
+  TRY(check_spans(fn, spans, 3, 9));
   cudaStream_t st = (cudaStream_t)stream;
   ON_DEVICE_OF(fn, workspace);
   CHECK_PTR(fn, x); CHECK_PTR(fn, w); CHECK_PTR(fn, targets); CHECK_PTR(fn, lse); CHECK_PTR(fn, dloss); CHECK_PTR(fn, dtok);

@@ -24,7 +24,8 @@ def test_scale_bytes():
     dict(x=None), dict(dtype=2), dict(ldx=99), dict(rows=-1), dict(cols=-1),
     dict(q=None, qt=None), dict(sc=None), dict(ldq=96), dict(ldq=104), dict(q=B + 8), dict(sc=C + 4),
     dict(sct=None), dict(ldqt=32), dict(ldqt=72), dict(qt=D + 1), dict(x=A + 2),
-    dict(rows=1 << 40),
+    dict(rows=1 << 40), dict(rows=(1 << 30) + 1, ldqt=1 << 31),
+    dict(q=A), dict(q=A + 800), dict(sc=B + 16), dict(qt=B + 64), dict(sct=A + 400), dict(sc=D + 4096),  # overlaps
 ])
 def test_quantize_refusals(bad):
     a = dict(x=A, dtype=g.DTYPE_F32, rows=50, cols=100, ldx=100, square=0, q=B, ldq=112, sc=C, qt=D, ldqt=64, sct=E)
@@ -41,7 +42,8 @@ def test_quantize_of_nothing_is_no_call():
 @pytest.mark.parametrize("bad", [
     dict(M=0), dict(N=0), dict(K=0), dict(a=None), dict(sa=None), dict(sb=None), dict(c=None), dict(lda=999),
     dict(lda=1016), dict(ldb=500), dict(ldc=519), dict(ldc=521), dict(out=2), dict(beta=1, out=g.DTYPE_BF16),
-    dict(a=A + 8), dict(c=C + 4), dict(sa=D + 8),
+    dict(a=A + 8), dict(c=C + 4), dict(sa=D + 8), dict(M=(1 << 30) + 1),
+    dict(c=A), dict(c=B + 4096), dict(c=D), dict(c=E - 4096),                                            # overlaps
 ])
 def test_gemm_refusals(bad):
     a = dict(M=777, N=520, K=1000, a=A, lda=1008, sa=D, b=B, ldb=1008, sb=E, out=g.DTYPE_F32, c=C, ldc=520, beta=0)
@@ -123,9 +125,25 @@ def test_ce_refusals(bad):
 @pytest.mark.parametrize("bad", [
     dict(lse=None), dict(dx=None, dw=None), dict(lddx=56), dict(lddw=56), dict(dloss=A, dtok=A), dict(dwt=2),
     dict(beta=1), dict(dx=E + 8), dict(lddx=68), dict(dw=E + 8), dict(lddw=68), dict(dtype=g.DTYPE_F32),
+    dict(dx=A), dict(dw=B), dict(dw=E), dict(dx=B + 128), dict(dx=D), dict(dw=C), dict(dw=WS), dict(dx=A + 64 * 20 - 16),
 ])
 def test_ce_backward_refusals(bad):
     assert ce_backward(**bad) == g.GPT_ERR_ARG
+
+
+def test_ce_forward_overlaps():
+    for bad in (A, B + 64, C, WS):
+        assert ce_forward(loss=bad) == g.GPT_ERR_ARG
+        assert "overlaps" in g.gpt_last_error()
+
+
+def test_columns_side_by_side_do_not_overlap():
+    """A gradient in the other half of rows that also hold its input is no overlap
+    (the call goes on to the device, which this machine does not have)."""
+    st = ce_backward(ldx=128, lddx=128, dx=A + 128, dw=None)
+    assert st != g.GPT_ERR_ARG or "overlaps" not in g.gpt_last_error()
+    assert ce_backward(ldx=128, lddx=128, dx=A + 112, dw=None) == g.GPT_ERR_ARG
+    assert "overlaps" in g.gpt_last_error()
 
 
 def test_ce_workspace():
