@@ -418,20 +418,20 @@ def grad_clip(grads, outs, max_norm, norm_out, workspace, ws_bytes, stream=None)
     norm_out (device float, or None), and the tensors scaled by min(1, max_norm /
     (norm + 1e-6)): in place (outs None) or into the tensors of outs, which
     have the same sizes and types.  max_norm = 0: no scaling."""
+    import torch
+    T = torch.Tensor
     global _clip_codes
     if _clip_codes is None:
-        import torch
         _clip_codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
-    types, sizes = [t.dtype for t in grads], [t.numel() for t in grads]
-    if not all([t.is_contiguous() for t in grads]) or not _clip_codes.keys() >= set(types):
+    types, sizes = [t.dtype for t in grads], list(map(T.numel, grads))
+    if not all(map(T.is_contiguous, grads)) or not _clip_codes.keys() >= set(types):
         raise ValueError("grad_clip: contiguous fp32 or bf16 tensors are wanted")
     out_ptrs = None
     if outs is not None:
-        if ([t.dtype for t in outs] != types or [t.numel() for t in outs] != sizes or
-                not all([t.is_contiguous() for t in outs])):
+        if [t.dtype for t in outs] != types or list(map(T.numel, outs)) != sizes or not all(map(T.is_contiguous, outs)):
             raise ValueError("grad_clip: the outputs differ from their tensors in number, type or size, or are not contiguous")
-        out_ptrs = array.array("Q", [t.data_ptr() for t in outs])
-    ptrs, ns = array.array("Q", [t.data_ptr() for t in grads]), array.array("q", sizes)
+        out_ptrs = array.array("Q", list(map(T.data_ptr, outs)))
+    ptrs, ns = array.array("Q", list(map(T.data_ptr, grads))), array.array("q", sizes)
     codes = array.array("i", [_clip_codes[t] for t in types])
     return _check(_lib.grad_clip(len(sizes), ptrs.buffer_info()[0], None if outs is None else out_ptrs.buffer_info()[0],
                                  ns.buffer_info()[0], codes.buffer_info()[0], float(max_norm), _ptr(norm_out),
