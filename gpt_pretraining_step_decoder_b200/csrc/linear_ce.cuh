@@ -14,7 +14,10 @@
 // mean's factor dloss / count, which the products apply in fp32: where few rows have a target in
 // common, dz = -(1 - p) with p near 0 is then exact instead of off by the same
 // half step in every row.  Three products of 2 N V d
-// operations bound it.  fp32: the same pieces through plain FFMA products, with
+// operations bound it.  B200, in a stream of calls: 32768 x 50304 x 768 forward
+// 1853 us (1366 TFLOP/s), 16384 x 65536 x 2048 backward with soft-cap 10.9 ms (1208
+// TFLOP/s, under the power cap; 9.4 ms in a short run), 33 x 50304 x 768 forward 23.5 us
+// (17.6 of them the one read of W, 4.4 TB/s).  fp32: the same pieces through plain FFMA products, with
 // fp32 logits of one piece at a time in the workspace.
 #pragma once
 #include "gemm_tc.cuh"
@@ -207,8 +210,9 @@ __global__ void __launch_bounds__(256) ce_piece_stats_kernel(const float* __rest
 // added in warp order.  Fewer tiles than SMs and a long K: K is also shared out
 // over blocks, whose tiles the last one to finish adds in share order.  A chunk
 // lies as [k][row ^ 8 (k / 4)], so that neither the writes of an operand that is
-// contiguous along k nor the reads conflict.  A small call is latency, a large one
-// the loads of the small tiles.
+// contiguous along k nor the reads conflict.  A small call is latency (256 x 512 x 128,
+// both launches: 12.2 us), a large one the loads of the small tiles (4096 x 8192 x
+// 1024: 6.3 ms, 33 TFLOP/s).
 struct CeProduct {
   const float* A; long long lda; int a_kmajor;
   const float* B; long long ldb; int b_kmajor;

@@ -32,6 +32,9 @@
  *     non-finite loss, a bounded wait that gave up) set a device error word
  *     instead of trapping; it is reported by the next gpt_sync_status() /
  *     ngram_sync_status().  gpt_last_error() gives a thread-local message.
+ *   - Workspaces: a call's scratch, free again when the call's work is done;
+ *     calls that may run at the same time (other streams, captured graphs that
+ *     are replayed side by side) need workspaces of their own.
  *   - Layouts: row-major; token ids and targets are int32 [B, T]; a target of
  *     -1 is ignored by the loss.  Linear weights are (out, in): y = x W^T.
  */
