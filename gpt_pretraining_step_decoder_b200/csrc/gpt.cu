@@ -527,7 +527,7 @@ struct GemmCtx {
 // Tile shape (256 or 128 columns, one SM or a pair) and K split of a bf16 product
 // with `any_tile` (the standalone cross entropy's, of any size): the form with
 // the least estimated time, fixed + waves * (k-blocks * c + e) + split, in
-// microseconds measured on B200.  A pair starts 1.2 us later and moves fewer bytes per
+// microseconds measured on B200.  A pair starts 1 us later and moves fewer bytes per
 // product once all SMs pull on L2 (33 x 50304 x 768: 24.4 us on pairs, 19.3 on one SM;
 // 32768 x 50304 x 768: 1618 and 1699); a split adds its second launch (on the
 // device and the host) and the partials' way through L2.  split_elems: room for fp32 partials (0: no split).
@@ -544,7 +544,7 @@ static TilePlan tile_plan(int M, int N, int K, long long split_elems) {
       for (int s = 1; s <= 16 && (s == 1 || (s <= room && kb / s >= 4)); ++s) {
         const double busy = std::min(1.0, (double)(tiles * s) / units);  // share of the SMs that load
         const double c = cg == 2 ? 0.34 : (bn == 256 ? 0.31 + 0.16 * busy : 0.30);
-        const double t = (cg == 2 ? 4.4 : 3.2) +
+        const double t = (cg == 2 ? 4.2 : 3.2) +
                          (double)cdiv_ll(tiles * s, units) * (cdiv(kb, s) * c + (bn == 256 ? 0.5 : 0.35)) +
                          (s > 1 ? 3.0 + (double)s * M * N * 8e-7 : 0.0);
         if (t < best_t) { best = TilePlan{bn, cg, s}; best_t = t; }

@@ -143,11 +143,11 @@ extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long
 //   fixed + waves * (k-blocks * c + e) + split,
 // in microseconds measured on B200 (launch to launch, over 23 shapes from 1 x 8 x
 // 16 to 8192 x 2048 x 16384; the choice is within 8% of the best form on each).  A
-// pair costs 1.2 us more to start and, with its one accumulator, more between
+// pair costs 1 us more to start and, with its one accumulator, more between
 // tiles, but moves fewer bytes per product once all SMs pull on L2: short
-// products run on one SM per tile (4096 x 4096 x 128: 9.4 us against 13.7 on
-// pairs, 200 x 768 x 768: 5.4 against 6.9), long ones on pairs (8192 x 2048 x 16384:
-// 206 against 245).  A split adds its second launch and the partials' way
+// products run on one SM per tile (4096 x 4096 x 128: 9.4 us against 10.6 on
+// pairs, 200 x 768 x 768: 5.4 against 6.4), long ones on pairs (8192 x 2048 x 16384:
+// 207 against 252).  A split adds its second launch and the partials' way
 // through L2; K is split in whole scale atoms (4 k-blocks).
 struct F8bPlan { int bn, cg, splits; };
 static F8bPlan f8b_plan(int M, int N, int K) {
@@ -162,10 +162,10 @@ static F8bPlan f8b_plan(int M, int N, int K) {
         const int share = cdiv(quads, s);
         if (cdiv(quads, share) != s) continue;  // the same shares as a smaller split
         const double busy = std::min(1.0, (double)(tiles * s) / units);  // share of the SMs that load
-        const double c = cg == 2 ? (bn == 256 ? 0.355 : 0.28) : (bn == 256 ? 0.31 + 0.16 * busy : 0.30);
-        const double e = cg == 2 ? (bn == 256 ? 1.75 : 1.3) : (bn == 256 ? 1.17 : 0.65);
+        const double c = cg == 2 ? (bn == 256 ? 0.345 : 0.30) : (bn == 256 ? 0.31 + 0.16 * busy : 0.30);
+        const double e = cg == 2 ? (bn == 256 ? 1.45 : 0.65) : (bn == 256 ? 1.17 : 0.65);
         const double waves = (double)((tiles * s + units - 1) / units);
-        const double t = (cg == 2 ? 4.4 : 3.2) + waves * (std::min(kb, 4 * share) * c + e) +
+        const double t = (cg == 2 ? 4.2 : 3.2) + waves * (std::min(kb, 4 * share) * c + e) +
                          (s > 1 ? 1.5 + (double)s * M * N * 8e-7 : 0.0);
         if (t < best_t) { best = F8bPlan{bn, cg, s}; best_t = t; }
       }
