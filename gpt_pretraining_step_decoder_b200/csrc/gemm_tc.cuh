@@ -143,6 +143,7 @@ struct Params {
   CUtensorMap tm_sfa, tm_sfb;
   int a_atoms, b_atoms;
   int n_run;   // K_LSE: column tiles in a row that one CTA (pair) takes of a row block
+  int k_chunk; // K_LSE: k-blocks accumulated in tensor memory before the sum moves on to registers
   int a_skip;  // bytes of a stage's A tile that are not loaded (a product of fewer than 128 rows)
 };
 
@@ -784,46 +785,52 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int split = RUNS ? 0 : (B3 ? t % per_product : t) % p.splits;
         const int kb0 = split * p.kb_per_split;
         const int kb1 = min(kb0 + p.kb_per_split, p.kb_total);
-        if (!warp_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.err)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!warp_wait(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
+        // one accumulator per chunk of K (K_LSE; else all of K is one chunk)
+        const int chunk = RUNS ? p.k_chunk : kb1 - kb0;
+        for (int kc = kb0; kc < kb1; kc += chunk) {
+          const int kc1 = min(kc + chunk, kb1);
+          if (!warp_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.err)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_base = smem_u32(sA + stage * C::A_BYTES);
-          const uint32_t b_base = smem_u32(sB + stage * C::B_BYTES);
-          uint32_t sfa = 0, sfb = 0, sid = 0;
-          if constexpr (F8 == 2) {
-            if ((kb & 3) == 0) {
-              sf_buf ^= 1u;
-              const uint32_t t0 = tmem_base + C::NACC * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
-              const uint32_t s0 = smem_u32(sSF + stage * C::SF_BYTES);
+          const uint32_t d_tmem = tmem_base + acc * BN;
+          for (int kb = kc; kb < kc1; ++kb) {
+            if (!warp_wait(&full[stage], phase, abort_flag, p.err)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a_base = smem_u32(sA + stage * C::A_BYTES);
+            const uint32_t b_base = smem_u32(sB + stage * C::B_BYTES);
+            uint32_t sfa = 0, sfb = 0, sid = 0;
+            if constexpr (F8 == 2) {
+              if ((kb & 3) == 0) {
+                sf_buf ^= 1u;
+                const uint32_t t0 = tmem_base + C::NACC * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
+                const uint32_t s0 = smem_u32(sSF + stage * C::SF_BYTES);
 #pragma unroll
-              for (int a = 0; a < 1 + C::SFB_ATOMS; ++a) tc_copy_scales_w<CG>(t0 + 4 * a, scale_desc(s0 + 512 * a));
+                for (int a = 0; a < 1 + C::SFB_ATOMS; ++a) tc_copy_scales_w<CG>(t0 + 4 * a, scale_desc(s0 + 512 * a));
+              }
+              sfa = tmem_base + C::NACC * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
+              sfb = sfa + 4;
+              sid = (uint32_t)(kb & 3);
             }
-            sfa = tmem_base + C::NACC * BN + sf_buf * 4 * (1 + C::SFB_ATOMS);
-            sfb = sfa + 4;
-            sid = (uint32_t)(kb & 3);
-          }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 32 bytes of K per instruction: 16 bf16 or 32 e4m3
-            const uint64_t ad = operand_desc(a_base, p.a_kmajor, k), bd = operand_desc(b_base, p.b_kmajor, k);
-            const uint32_t acc_in = (kb > kb0 || k > 0) ? 1u : 0u;
-            if constexpr (F8 == 2)
-              tc_mma_scaled_w<CG>(d_tmem, ad, bd, idesc | (sid << 4) | (sid << 29), acc_in, sfa, sfb);
-            else if constexpr (CG == 2 && F8) tc_mma_pair_f8_w(d_tmem, ad, bd, idesc, acc_in);
-            else if constexpr (CG == 2) tc_mma_pair_w(d_tmem, ad, bd, idesc, acc_in);
-            else if constexpr (F8) tc_mma_f8_w(d_tmem, ad, bd, idesc, acc_in);
-            else tc_mma_w(d_tmem, ad, bd, idesc, acc_in);
+            for (int k = 0; k < 4; ++k) {  // 32 bytes of K per instruction: 16 bf16 or 32 e4m3
+              const uint64_t ad = operand_desc(a_base, p.a_kmajor, k), bd = operand_desc(b_base, p.b_kmajor, k);
+              const uint32_t acc_in = (kb > kc || k > 0) ? 1u : 0u;
+              if constexpr (F8 == 2)
+                tc_mma_scaled_w<CG>(d_tmem, ad, bd, idesc | (sid << 4) | (sid << 29), acc_in, sfa, sfb);
+              else if constexpr (CG == 2 && F8) tc_mma_pair_f8_w(d_tmem, ad, bd, idesc, acc_in);
+              else if constexpr (CG == 2) tc_mma_pair_w(d_tmem, ad, bd, idesc, acc_in);
+              else if constexpr (F8) tc_mma_f8_w(d_tmem, ad, bd, idesc, acc_in);
+              else tc_mma_w(d_tmem, ad, bd, idesc, acc_in);
+            }
+            if constexpr (CG == 2) tc_commit_pair_w(&empty[stage]);
+            else tc_commit_w(&empty[stage]);
+            if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
           }
-          if constexpr (CG == 2) tc_commit_pair_w(&empty[stage]);
-          else tc_commit_w(&empty[stage]);
-          if (++stage == C::STAGES) { stage = 0; phase ^= 1; }
+          if (!ok) break;
+          if constexpr (CG == 2) tc_commit_pair_w(&tfull[acc]);
+          else tc_commit_w(&tfull[acc]);
+          if (++acc == C::NACC) { acc = 0; acc_phase ^= 1; }
         }
         if (!ok) break;
-        if constexpr (CG == 2) tc_commit_pair_w(&tfull[acc]);
-        else tc_commit_w(&tfull[acc]);
-        if (++acc == C::NACC) { acc = 0; acc_phase ^= 1; }
       }
     }
   } else {
@@ -948,6 +955,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if constexpr (KM == K_LSE) {
+        // The tensor cores' fp32 accumulation truncates, always towards zero, so the
+        // largest logits of a long K come out low (lse off by 1.2e-6 of its value at
+        // d = 1900): K goes through tensor memory in chunks whose sums are added
+        // here, rounded to nearest.  The accumulators take turns, so the
+        // next chunk is multiplied meanwhile.
+        for (int kc = p.k_chunk; kc < p.kb_total; kc += p.k_chunk) {
+          if (++acc == C::NACC) { acc = 0; acc_phase ^= 1; }
+          if (!warp_wait(&tfull[acc], acc_phase, abort_flag, p.err)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t tr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN + ccol;
+#pragma unroll
+          for (int q2 = 0; q2 < HALF / 32; ++q2) {
+            uint32_t r[32];
+            tmem_ld32_nowait(tr + q2 * 32, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) accr[q2 * 32 + i] += __uint_as_float(r[i]) * ealpha;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (CG == 2) mbar_arrive_cluster(tempty0 + acc * 8);
+            else mbar_arrive(&tempty[acc]);
+          }
+        }
+        if (!ok) break;
         // the half tile's row maximum and sum of exp(z - max), all from
         // registers: nothing but these two numbers leaves the tile
         if (e.softcap > 0.f) softcap_block<HALF>(accr, e.softcap);

@@ -320,6 +320,7 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
   if (splits > p.kb_total) splits = p.kb_total;
   p.kb_per_split = cdiv(p.kb_total, splits);
   p.splits = cdiv(p.kb_total, p.kb_per_split);
+  p.k_chunk = cdiv(p.kb_total, cdiv(p.kb_total, 16));  // at most 1024 of K
   p.epi = e;
   p.partial = partial;
   p.err = err;
@@ -422,7 +423,7 @@ static int gemm_f8_launch(int M, int N, int K, const uint8_t* A, long long lda, 
   }
   tc::Params p;
   p.M = M; p.N = N; p.K = K; p.batch = 1;
-  p.a_skip = 0; p.n_run = 1;
+  p.a_skip = 0; p.n_run = 1; p.k_chunk = 0;
   p.a_kmajor = 1; p.b_kmajor = 1;
   p.m_tiles = cdiv(M, CG * tc::BM);
   p.n_tiles = cdiv(N, 256);

@@ -190,7 +190,7 @@ static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda,
   TRY(make_tmap_gen(&p.tm_sfa, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sa, dsa, ls, bsa, CU_TENSOR_MAP_SWIZZLE_NONE));
   TRY(make_tmap_gen(&p.tm_sfb, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sb, dsb, ls, bsb, CU_TENSOR_MAP_SWIZZLE_NONE));
   p.a_atoms = cdiv(M, 128); p.b_atoms = cdiv(N, 128);
-  p.a_skip = 0; p.n_run = 1;
+  p.a_skip = 0; p.n_run = 1; p.k_chunk = 0;
   p.M = M; p.N = N; p.K = K; p.batch = 1;
   p.a_kmajor = 1; p.b_kmajor = 1;
   p.m_tiles = cdiv(M, CG * tc::BM);

@@ -123,7 +123,7 @@ class Case:
             assert (err <= tol + 1e-30).all(), (err.max(), np.argwhere(err > tol)[:3])
 
 
-SHAPES = [(1, 64, 8), (1, 1, 8), (33, 1000, 64), (5000, 300, 64), (128, 256, 128), (130, 513, 72), (257, 4160, 128), (300, 5003, 256), (5, 50257, 64)]
+SHAPES = [(1, 64, 8), (1, 1, 8), (33, 1000, 64), (5000, 300, 64), (70, 300, 1096), (300, 520, 2056), (128, 256, 128), (130, 513, 72), (257, 4160, 128), (300, 5003, 256), (5, 50257, 64)]
 
 
 @pytest.mark.parametrize("softcap", [0.0, 15.0])
