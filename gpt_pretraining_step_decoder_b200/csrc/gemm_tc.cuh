@@ -55,8 +55,8 @@
 // registers, 128-column tiles two.  (192-column tiles with two accumulators lose:
 // L2 to shared memory bounds the e4m3 products, about 10 TB/s over the GPU, and
 // they need 17% more bytes per product: 8192 x 2048 x 16384 309 us against 227.)
-// B200: 8192 x 2048 x 16384 205 us in a short run (2.7 PFLOP/s), 243 under the power
-// cap; 32768 x 2304 x 768 65 us, of which its 151 MB of output alone take 41.
+// B200: 8192 x 2048 x 16384 202 us in a short run (2.7 PFLOP/s), 242 under the power
+// cap; 32768 x 2304 x 768 59 us, of which its 151 MB of output alone take 41.
 //
 // K-major and MN-major operands are both read straight from their
 // row-major buffers (the UMMA descriptor's major-ness bit), so forward,
