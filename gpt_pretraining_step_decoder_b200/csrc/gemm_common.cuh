@@ -75,6 +75,21 @@ struct GemmEpilogue {
   unsigned* counter;  // EPI_LSE: set to 0 (the next kernel's count of finished blocks)
 };
 
+// One thread's count of the targets in [0, vocab) among n, of `threads` that
+// share them; eight loads in flight.
+__device__ __forceinline__ int count_targets(const int32_t* __restrict__ targets, int n, int vocab, int thread,
+                                             int threads) {
+  int c = 0;
+  for (int i0 = thread; i0 < n; i0 += 8 * threads) {
+    int y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = i0 + k * threads < n ? targets[i0 + k * threads] : -1;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) c += y[k] >= 0 && y[k] < vocab;
+  }
+  return c;
+}
+
 template <typename act_t>
 __device__ __forceinline__ void epi_apply_one(const GemmEpilogue& e, long long m, long long n,
                                               float acc) {

@@ -854,12 +854,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // while its first tile is multiplied
       if (blockIdx.x == 0 && e.base_out != nullptr) {
         int* counts = reinterpret_cast<int*>(sturns);
-        int c = 0;
-        for (int i = ew * 32 + lane; i < p.M; i += 32 * EPI_WARPS) {
-          const int y = e.targets[i];
-          c += y >= 0 && y < e.vocab;
-        }
-        c = __reduce_add_sync(0xffffffffu, c);
+        int c = __reduce_add_sync(0xffffffffu, count_targets(e.targets, p.M, e.vocab, ew * 32 + lane, 32 * EPI_WARPS));
         if (lane == 0) counts[ew] = c;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * EPI_WARPS) : "memory");
         if (ew == 0 && lane == 0) {

@@ -146,9 +146,7 @@ struct CeRowScale {
 __device__ __forceinline__ float ce_scale_base(const CeRowScale& a) {
   if (a.dtok) return 0.f;
   __shared__ int sh[32];
-  int c = 0;
-  for (int i = threadIdx.x; i < a.N; i += blockDim.x) { const int y = a.targets[i]; c += y >= 0 && y < a.V; }
-  c = __reduce_add_sync(0xffffffffu, c);
+  int c = __reduce_add_sync(0xffffffffu, count_targets(a.targets, a.N, a.V, threadIdx.x, blockDim.x));
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = c;
   __syncthreads();
   c = 0;
