@@ -461,7 +461,8 @@ int fp8_block_scale_bytes(long long rows, long long cols, size_t* bytes);
 int fp8_block_quantize(const void* x, int dtype, long long rows, long long cols, long long ldx, int square, uint8_t* q,
                        long long ldq, uint8_t* scales, uint8_t* qt, long long ldqt, uint8_t* scales_t, void* stream);
 
-/* Device workspace bytes gptx_gemm_fp8_block() needs (0 when K is not split). */
+/* Device workspace bytes gptx_gemm_fp8_block() needs (0 when K is not split),
+ * with the tile forms in force at the time (gptx_set_gemm_cta_pairs). */
 int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes);
 
 /*
@@ -487,7 +488,7 @@ int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long long lda, co
  * linear_ce_backward() (backward != 0).  vocab_piece: columns of the vocabulary
  * taken at a time (0 = chosen, about 512 MB for N rows of them; the bf16
  * forward pass keeps no logits at all and takes none).  Pass the same value to
- * the call.
+ * the call.  Counts the tile forms in force at the time (gptx_set_gemm_cta_pairs).
  */
 int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int vocab_piece, size_t* bytes);
 

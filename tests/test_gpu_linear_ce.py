@@ -153,7 +153,8 @@ def test_backward_bf16(g, N, V, d, softcap, piece, pairs):
 
 @pytest.mark.parametrize("piece", [0, 64])
 @pytest.mark.parametrize("softcap", [0.0, 15.0])
-@pytest.mark.parametrize("N,V,d", [(1, 1, 1), (1, 7, 3), (33, 100, 17), (65, 513, 64), (130, 300, 129)])
+@pytest.mark.parametrize("N,V,d", [(1, 1, 1), (1, 7, 3), (33, 100, 17), (65, 513, 64), (130, 300, 129), (513, 2300, 130),
+                                   (1000, 1300, 72)])
 def test_fp32(g, N, V, d, softcap, piece):
     c = Case(N, V, d, "f32", softcap)
     c.check_forward(c.forward(g, piece))
