@@ -90,7 +90,15 @@ enum KMode {
   K_LSE,          // no output: row statistics of z = softcap(acc) per half tile, target logit
   K_DLOGITS,      // bf16 gradient of the cross entropy with respect to the logits
   K_AXPBY,        // bf16 acc + aux_scale * aux (aux streamed like the ReLU^2 backward's)
+  // The same two for caps above WIDE_CAP (tanh_block).  Kernels of their own: with
+  // the series beside the quick form, the loss of 32768 x 50304 x 768 without a cap
+  // went from 1770 to 1840 us (registers).
+  K_LSE_WIDE,
+  K_DLOGITS_WIDE,
 };
+__host__ __device__ constexpr bool is_lse(int km) { return km == K_LSE || km == K_LSE_WIDE; }
+__host__ __device__ constexpr bool is_dlogits(int km) { return km == K_DLOGITS || km == K_DLOGITS_WIDE; }
+constexpr float WIDE_CAP = 64.f;
 
 // The ReLU^2-backward epilogue streams activations through a ring of its
 // own, which costs a pipeline stage; every other epilogue uses the light
@@ -527,6 +535,42 @@ __device__ __forceinline__ void softcap_block(float (&v)[NVAL], float cap) {
   for (int i = 0; i < NVAL; ++i) v[i] = cap * (1.f - __fdividef(2.f, __expf(v[i] * two_over_cap) + 1.f));
 }
 
+// v -> tanh(v / cap) for a block of logits (the standalone cross entropy's
+// epilogues): 1 - 2 / (exp(2 v / cap) + 1) from the two approximate units alone
+// (the ends come out as +-1).  Its error of about 2^-22 is absolute, so the logit
+// is off by cap 2^-22: 1.5e-5 at WIDE_CAP = 64, but 0.2 at 10^6.  Above it (WIDE) the
+// quotients below 1/2 take tanh's Taylor series through the 13th power (next
+// term 9e-8 of the value there), whose error is relative.  Through __expf and
+// __fdividef, as softcap_block, the loss of 32768 x 50304 x 768 with a cap took 2164 us
+// instead of 2131, the gradient of 16384 x 65536 x 2048 11015 instead of 10922; WIDE's
+// loss takes 3430 us (12 more instructions an element).
+template <int NVAL, bool WIDE>
+__device__ __forceinline__ void tanh_block(float (&v)[NVAL], float cap) {
+  const float c = 2.f * 1.4426950408889634f / cap;
+  auto quick = [](float x) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.f));
+    return fmaf(-2.f, r, 1.f);
+  };
+  if constexpr (!WIDE) {
+#pragma unroll
+    for (int i = 0; i < NVAL; ++i) v[i] = quick(v[i] * c);
+  } else {
+    const float rc = 1.f / cap;
+#pragma unroll
+    for (int i = 0; i < NVAL; ++i) {
+      const float u = v[i] * rc, s = u * u;
+      float t = fmaf(s, 21844.f / 6081075.f, -1382.f / 155925.f);
+      t = fmaf(s, t, 62.f / 2835.f);
+      t = fmaf(s, t, -17.f / 315.f);
+      t = fmaf(s, t, 2.f / 15.f);
+      t = fmaf(s, t, -1.f / 3.f);
+      v[i] = fabsf(u) < 0.5f ? fmaf(u * s, t, u) : quick(v[i] * c);
+    }
+  }
+}
+
 // Output tile (m-block, n-block) of linear tile index mn.  Tiles come in
 // groups of group_m m-blocks; inside a group the m-block varies fastest, so
 // the CTAs running at one time cover about group_m x (SMs / group_m) tiles
@@ -638,7 +682,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
   const int unit = blockIdx.x / CG, n_units = gridDim.x / CG;
   // this CTA's (pair's) walk over the tiles
-  constexpr bool RUNS = KM == K_LSE;
+  constexpr bool RUNS = is_lse(KM);
   const int t_first = RUNS ? 0 : unit, t_step = RUNS ? 1 : n_units;
   const int t_end = RUNS ? run_walk(unit, n_units, p) : tiles;
 
@@ -680,7 +724,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // so far only shared and tensor memory: set up while the kernel before this
   // one in the stream still finishes
   pdl_wait();
-  if constexpr (KM == K_LSE)
+  if constexpr (is_lse(KM))
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.epi.counter = 0u;
   if constexpr (KM == K_QKV) {
     if (threadIdx.x < 64 && p.epi.rope != nullptr) sturns[threadIdx.x] = p.epi.rope[threadIdx.x];
@@ -849,7 +893,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     float ealpha = e.alpha;
     if constexpr (F8 == 1 || (F8 == 0 && (KM == K_STORE || KM == K_STORE_F32 || KM == K_REDUCE_F32 || KM == K_PARTIAL)))
       ealpha *= (e.scale_a ? *e.scale_a : 1.f) * (e.scale_b ? *e.scale_b : 1.f);
-    if constexpr (KM == K_DLOGITS) {
+    if constexpr (is_dlogits(KM)) {
       // the mean's gradient scale, counted by the first CTA's epilogue warps
       // while its first tile is multiplied
       if (blockIdx.x == 0 && e.base_out != nullptr) {
@@ -911,7 +955,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float row_lse = 0.f, row_g = 0.f;
       const uint32_t trow = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN + ccol;
       int ytgt = -1;
-      if constexpr (KM == K_DLOGITS) {
+      if constexpr (is_dlogits(KM)) {
         if (m < p.M) {
           const int y = e.targets[m];
           row_lse = e.lse[m];
@@ -923,7 +967,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
       }
-      if constexpr (KM == K_LSE) ytgt = m < p.M ? e.targets[m] : -1;
+      if constexpr (is_lse(KM)) ytgt = m < p.M ? e.targets[m] : -1;
       // The store, ReLU^2 and fp32 epilogues take the warp's whole half tile
       // from TMEM into registers at once and hand the accumulator back to the
       // MMA warp before any arithmetic or store, so the MMA of the tile after
@@ -949,7 +993,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           else mbar_arrive(&tempty[acc]);
         }
       }
-      if constexpr (KM == K_LSE) {
+      if constexpr (is_lse(KM)) {
         // The tensor cores' fp32 accumulation truncates, always towards zero, so the
         // largest logits of a long K come out low (lse off by 1.2e-6 of its value at
         // d = 1900): K goes through tensor memory in chunks whose sums are added
@@ -978,7 +1022,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         // the half tile's row maximum and sum of exp(z - max), all from
         // registers: nothing but these two numbers leaves the tile
-        if (e.softcap > 0.f) softcap_block<HALF>(accr, e.softcap);
+        if (e.softcap > 0.f) {
+          tanh_block<HALF, KM == K_LSE_WIDE>(accr, e.softcap);
+#pragma unroll
+          for (int i = 0; i < HALF; ++i) accr[i] *= e.softcap;
+        }
         const int nv = p.N - n0;  // columns of the half tile that exist
         if (nv < HALF) {
 #pragma unroll
@@ -1168,21 +1216,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
           rsum += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
-        } else if constexpr (KM == K_DLOGITS) {
+        } else if constexpr (is_dlogits(KM)) {
           // (exp(z - lse) - [target]) * scale; the exponent's argument stays a
           // difference of fp32 numbers, two at a time
           constexpr float L2E = 1.4426950408889634f;
           const float nb = -row_lse * L2E;
           const int yo = ytgt - nc;
           if (e.softcap > 0.f) {
-            softcap_block<64>(v, e.softcap);
-            const float rc = 1.f / e.softcap;
+            // t = z / softcap, so z log2 e = t (softcap log2 e) and the slope is 1 - t^2
+            tanh_block<64, KM == K_DLOGITS_WIDE>(v, e.softcap);
+            const float cl = e.softcap * L2E;
+            float tgt = 0.f;
+            if (yo >= 0 && yo < 64 && row_g != 0.f) {  // rare: the target's own term
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              const float t = v[i] * rc;
-              float pr;
-              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(pr) : "f"(fmaf(v[i], L2E, nb)));
-              v[i] = row_g != 0.f ? (pr - (i == yo ? 1.f : 0.f)) * fmaf(-t, t, 1.f) * row_g : 0.f;
+              for (int i = 0; i < 64; ++i) tgt = (i == yo) ? fmaf(-v[i], v[i], 1.f) * row_g : tgt;
+            }
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              float x0, x1, p0, p1;
+              fma2(x0, x1, v[i], v[i + 1], cl, nb);
+              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p0) : "f"(x0));
+              asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p1) : "f"(x1));
+              const float g0 = fmaf(-v[i], v[i], 1.f) * row_g, g1 = fmaf(-v[i + 1], v[i + 1], 1.f) * row_g;
+              v[i] = row_g != 0.f ? p0 * g0 : 0.f;  // a row without a gradient stays out, whatever its logits
+              v[i + 1] = row_g != 0.f ? p1 * g1 : 0.f;
+            }
+            if (yo >= 0 && yo < 64) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i] -= (i == yo) ? tgt : 0.f;
             }
           } else {
 #pragma unroll
@@ -1272,7 +1333,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         return true;
       };
-      if constexpr (PRE && KM != K_LSE) {
+      if constexpr (PRE && !is_lse(KM)) {
 #pragma unroll
         for (int c = 0; c < HALF / CW; ++c) {
           if (c >= nblk) break;  // warp-uniform
@@ -1281,7 +1342,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int i = 0; i < CW; ++i) v[i] = accr[c * CW + i];
           if (!out_block(c, v)) { ok = false; break; }
         }
-      } else if constexpr (KM != K_QKV && KM != K_LSE) {
+      } else if constexpr (KM != K_QKV && !is_lse(KM)) {
 #pragma unroll 1
         for (int c = 0; c < nblk; ++c) {
           float v[64];

@@ -363,8 +363,8 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
   else if (e.mode == EPI_DRELU2) km = tc::K_DRELU2;
   else if (e.mode == EPI_QKV) km = tc::K_QKV;
   else if (e.mode == EPI_AXPBY) km = tc::K_AXPBY;
-  else if (e.mode == EPI_LSE) km = tc::K_LSE;
-  else if (e.mode == EPI_DLOGITS) km = tc::K_DLOGITS;
+  else if (e.mode == EPI_LSE) km = e.softcap > tc::WIDE_CAP ? tc::K_LSE_WIDE : tc::K_LSE;
+  else if (e.mode == EPI_DLOGITS) km = e.softcap > tc::WIDE_CAP ? tc::K_DLOGITS_WIDE : tc::K_DLOGITS;
   else km = tc::K_LOGITS;
   if (km == tc::K_QKV && BN != 256) return fail(GPT_ERR_ARG, "QKV epilogue needs 256-column tiles (N >= 256)");
   if (b3) {
@@ -392,7 +392,9 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
     case tc::K_QKV: TRY((gemm_tc_launch_k<BN, tc::K_QKV, CG>(ta, tb, tcm, taux, p, st))); break;
     case tc::K_AXPBY: TRY((gemm_tc_launch_k<BN, tc::K_AXPBY, CG>(ta, tb, tcm, taux, p, st))); break;
     case tc::K_LSE: TRY((gemm_tc_launch_k<BN, tc::K_LSE, CG>(ta, tb, tcm, taux, p, st))); break;
+    case tc::K_LSE_WIDE: TRY((gemm_tc_launch_k<BN, tc::K_LSE_WIDE, CG>(ta, tb, tcm, taux, p, st))); break;
     case tc::K_DLOGITS: TRY((gemm_tc_launch_k<BN, tc::K_DLOGITS, CG>(ta, tb, tcm, taux, p, st))); break;
+    case tc::K_DLOGITS_WIDE: TRY((gemm_tc_launch_k<BN, tc::K_DLOGITS_WIDE, CG>(ta, tb, tcm, taux, p, st))); break;
     default: TRY((gemm_tc_launch_k<BN, tc::K_LOGITS, CG>(ta, tb, tcm, taux, p, st))); break;
   }
   }

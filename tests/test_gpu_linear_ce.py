@@ -324,3 +324,38 @@ def test_gradient_against_differences(g):
         want = (grad.double() * v.double()).sum().item()
         # third-order term: |v|^3 h^2 / 6 of a loss whose third derivative is below 1 per logit
         assert abs((up - down) / (2 * h) / count - want) <= 5e-3 * max(1.0, abs(want))
+
+
+class WideCap(Case):
+    """A cap far above the logits: there z is nearly v, and its error has to stay a
+    part of z, not of the cap (the quotient's series is right to 2^-21 of tanh; the
+    exponential's form, from a half on, to 2^-22 of 1: 2^-20 of z, doubled here)."""
+
+    def ez(self):
+        z = np.abs(ce.logits(self.x, self.w, self.cap))
+        return (self.d + 16) * 2.0 ** -23 * (np.abs(self.x) @ np.abs(self.w).T) + z * 2.0 ** -19
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("cap,spread", [(65.0, 2.0), (100.0, 150.0), (1e4, 2.0), (1e6, 2.0), (1e20, 2.0)])
+@pytest.mark.parametrize("N,V,d", [(33, 1000, 64), (300, 520, 2056)])
+def test_wide_softcap(g, N, V, d, cap, spread, dtype):
+    c = WideCap(N, V, d, dtype=dtype, softcap=cap, spread=spread)
+    c.check_forward(c.forward(g))
+    c.check_backward(*c.backward(g, dloss=1.5), dloss=1.5)
+    assert g.ngram_sync_status() == g.GPT_OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cap", [0.0, 15.0, 100.0])
+def test_row_of_nan_with_a_zero_gradient(g, cap, dtype):
+    """A per-token gradient of 0 keeps a NaN row out of dx, its target's term too."""
+    import torch
+    c = Case(60, 300, 64, dtype, softcap=cap, ignored=0.0)
+    c.xd[7, :c.d] = float("nan")
+    lse = c.forward(g)[2]
+    dtok = np.ones(60, dtype=np.float32)
+    dtok[7] = 0
+    gx, _ = c.backward(g, dtok=dtok, dw=False, lse=lse)
+    assert not gx[7].any() and torch.isfinite(gx).all()
+    g.ngram_sync_status()
