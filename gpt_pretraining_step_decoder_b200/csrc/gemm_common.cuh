@@ -73,6 +73,7 @@ struct GemmEpilogue {
   float* base_out;
   int vocab, col0;
   unsigned* counter;  // EPI_LSE: set to 0 (the next kernel's count of finished blocks)
+  int n_run;          // EPI_LSE: column tiles in a row that one CTA (pair) takes of a row block
 };
 
 // One thread's count of the targets in [0, vocab) among n, of `threads` that

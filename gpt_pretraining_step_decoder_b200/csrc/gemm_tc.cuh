@@ -150,7 +150,6 @@ struct Params {
   // row atoms per k-quad
   CUtensorMap tm_sfa, tm_sfb;
   int a_atoms, b_atoms;
-  int n_run;   // K_LSE: column tiles in a row that one CTA (pair) takes of a row block
   int k_chunk; // K_LSE: k-blocks accumulated in tensor memory before the sum moves on to registers
   int a_skip;  // bytes of a stage's A tile that are not loaded (a product of fewer than 128 rows)
 };
@@ -593,14 +592,14 @@ __device__ __forceinline__ void tile_coords(int mn, const Params& p, int& mt, in
 // tile t % n_run of its run; the row block varies fastest over the runs, so the
 // units share the same columns of B.  False where a run ends past the last tile.
 __device__ __forceinline__ bool run_coords(int t, int unit, int n_units, const Params& p, int& mt, int& nt) {
-  const int item = unit + t / p.n_run * n_units;
+  const int item = unit + t / p.epi.n_run * n_units;
   mt = item % p.m_tiles;
-  nt = item / p.m_tiles * p.n_run + t % p.n_run;
+  nt = item / p.m_tiles * p.epi.n_run + t % p.epi.n_run;
   return nt < p.n_tiles;
 }
 __device__ __forceinline__ int run_walk(int unit, int n_units, const Params& p) {
-  const int items = p.m_tiles * ((p.n_tiles + p.n_run - 1) / p.n_run);
-  return unit < items ? ((items - 1 - unit) / n_units + 1) * p.n_run : 0;
+  const int items = p.m_tiles * ((p.n_tiles + p.epi.n_run - 1) / p.epi.n_run);
+  return unit < items ? ((items - 1 - unit) / n_units + 1) * p.epi.n_run : 0;
 }
 
 // byte offset of 16-byte chunk j of row r in a 128-byte-swizzled block
@@ -1057,7 +1056,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         rsum = ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
         // join the run's earlier tiles; the run's last tile writes the pair
-        if (t % p.n_run != 0) {
+        if (t % p.epi.n_run != 0) {
           const float mj = fmaxf(rmax, run_max);
           if (mj != -INFINITY) {
             rsum = rsum * __expf(rmax - mj) + run_sum * __expf(run_max - mj);
@@ -1066,8 +1065,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         run_max = rmax;
         run_sum = rsum;
-        if ((t + 1) % p.n_run == 0 || nt + 1 == p.n_tiles) {
-          if (m < p.M) e.stats[(long long)(nt / p.n_run * 2 + (ew >> 2)) * p.M + m] = make_float2(rmax, rsum);
+        if ((t + 1) % p.epi.n_run == 0 || nt + 1 == p.n_tiles) {
+          if (m < p.M) e.stats[(long long)(nt / p.epi.n_run * 2 + (ew >> 2)) * p.M + m] = make_float2(rmax, rsum);
         }
       }
       if constexpr (KM == K_LOGITS) {

@@ -271,8 +271,8 @@ static int make_tmap3(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t 
 // where there is a single row block (as even as tiles go, and the fewest pairs to
 // join), else 4 where that leaves the units many runs each (their last wave is then
 // a small part), else 1.
-static int lse_run(int M, int N, int BN, int cg) {
-  const int m = cdiv(M, 128 * cg), n = cdiv(N, BN), units = device_sms() / cg;
+static int lse_run(int M, int N, int BN, int cg, int sms) {
+  const int m = cdiv(M, 128 * cg), n = cdiv(N, BN), units = sms / cg;
   if (m <= 1) return std::max(1, cdiv(n, units));
   return (long long)m * n >= 128LL * units ? 4 : 1;
 }
@@ -306,7 +306,6 @@ static int gemm_tc_launch(int M, int N, int K, GemmOperand A, GemmOperand B, Gem
   p.batch = bt.n;
   p.a_kmajor = A.kmajor; p.b_kmajor = B.kmajor;
   p.a_skip = (tc::BM - a_rows) * tc::BK * 2;
-  p.n_run = e.mode == EPI_LSE ? lse_run(M, N, BN, CG) : 1;
   p.m_tiles = cdiv(M, CG * tc::BM);
   p.n_tiles = cdiv(N, BN);
   // n-fastest order while the whole B operand stays in L2; grouped m-blocks
@@ -425,7 +424,7 @@ static int gemm_f8_launch(int M, int N, int K, const uint8_t* A, long long lda, 
   }
   tc::Params p;
   p.M = M; p.N = N; p.K = K; p.batch = 1;
-  p.a_skip = 0; p.n_run = 1; p.k_chunk = 0;
+  p.a_skip = 0; p.k_chunk = 0;
   p.a_kmajor = 1; p.b_kmajor = 1;
   p.m_tiles = cdiv(M, CG * tc::BM);
   p.n_tiles = cdiv(N, 256);
@@ -524,20 +523,20 @@ struct GemmCtx {
   unsigned* err;
   cudaStream_t st;
   Prof* prof;
-  bool any_tile = false;  // tile shape and split by tile_plan
 };
 
-// Tile shape (256 or 128 columns, one SM or a pair) and K split of a bf16 product
-// with `any_tile` (the standalone cross entropy's, of any size): the form with
+// Tile shape (256 or 128 columns, one SM or a pair) and K split of a bf16 product of
+// any size (the standalone cross entropy's) on a device of `sms` SMs: the form with
 // the least estimated time, fixed + waves * (k-blocks * c + e) + split, in
 // microseconds measured on B200.  A pair starts 1 us later and moves fewer bytes per
 // product once all SMs pull on L2 (33 x 50304 x 768: 24.4 us on pairs, 19.3 on one SM;
 // 32768 x 50304 x 768: 1618 and 1699); a split adds its second launch (on the
 // device and the host) and the partials' way through L2.  split_elems: room for fp32 partials (0: no split).
-struct TilePlan { int bn, cg, splits; };
-static TilePlan tile_plan(int M, int N, int K, long long split_elems) {
-  const int kb = cdiv(K, 64), sms = device_sms();
-  TilePlan best{128, 1, 1};
+// n_run: lse_run's, for an EPI_LSE product.
+struct TilePlan { int bn, cg, splits, n_run; };
+static TilePlan tile_plan(int M, int N, int K, long long split_elems, int sms) {
+  const int kb = cdiv(K, 64);
+  TilePlan best{128, 1, 1, 1};
   double best_t = 1e300;
   for (int cg = 1; cg <= (M > 128 && N >= 256 && gemm_pairs_enabled() ? 2 : 1); ++cg)
     for (int bn : {256, 128}) {
@@ -550,15 +549,27 @@ static TilePlan tile_plan(int M, int N, int K, long long split_elems) {
         const double t = (cg == 2 ? 4.2 : 3.2) +
                          (double)cdiv_ll(tiles * s, units) * (cdiv(kb, s) * c + (bn == 256 ? 0.5 : 0.35)) +
                          (s > 1 ? 3.0 + (double)s * M * N * 8e-7 : 0.0);
-        if (t < best_t) { best = TilePlan{bn, cg, s}; best_t = t; }
+        if (t < best_t) { best = TilePlan{bn, cg, s, 1}; best_t = t; }
       }
     }
   return best;
 }
+static TilePlan lse_plan(int M, int N, int K, int sms) {
+  TilePlan t = tile_plan(M, N, K, 0, sms);
+  t.n_run = lse_run(M, N, t.bn, t.cg, sms);
+  return t;
+}
 // Pairs of statistics per row that an EPI_LSE product leaves (two per run of tiles).
-static int lse_pairs(int M, int N, int K) {
-  const TilePlan t = tile_plan(M, N, K, 0);
-  return 2 * cdiv(cdiv(N, t.bn), lse_run(M, N, t.bn, t.cg));
+static int lse_pairs(int N, const TilePlan& t) { return 2 * cdiv(cdiv(N, t.bn), t.n_run); }
+
+// A bf16 product in the form of `t`.  The plan is the caller's: what it sized by
+// the plan has to match the launch even if gptx_set_gemm_cta_pairs is called meanwhile.
+static int gemm_planned(const GemmCtx& g, const TilePlan& t, int M, int N, int K, GemmOperand A, GemmOperand B,
+                        GemmEpilogue e) {
+  e.n_run = t.n_run;
+  if (t.cg == 2) return gemm_tc_launch<256, 2>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
+  if (t.bn == 256) return gemm_tc_launch<256>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
+  return gemm_tc_launch<128>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
 }
 
 static int gemm(const GemmCtx& g, int M, int N, int K, GemmOperand A, GemmOperand B, GemmEpilogue e,
@@ -571,7 +582,7 @@ static int gemm(const GemmCtx& g, int M, int N, int K, GemmOperand A, GemmOperan
     return GPT_OK;
   }
   const bool f32out = e.mode == EPI_ACCUM_F32 || e.mode == EPI_STORE_F32;
-  const bool split_ok = allow_split && (f32out || e.mode == EPI_STORE);
+  const bool split_ok = allow_split && f32out;
   auto splits_for = [&](int bn, int cg = 1) {
     if (!split_ok) return 1;
     int s = pick_splits(M, N, K, bn, cg);
@@ -583,12 +594,6 @@ static int gemm(const GemmCtx& g, int M, int N, int K, GemmOperand A, GemmOperan
   // statistics and the ReLU^2 backward's activation stream), which measured
   // faster on one-SM tiles (B200: LM-head logits 2.55 vs 2.79 ms, ReLU^2
   // backward 2.04 vs 2.17 ms per GPT-2-small step)
-  if (g.any_tile) {
-    const TilePlan t = tile_plan(M, N, K, split_ok ? g.splitk_elems : 0);
-    if (t.cg == 2) return gemm_tc_launch<256, 2>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
-    if (t.bn == 256) return gemm_tc_launch<256>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
-    return gemm_tc_launch<128>(M, N, K, A, B, e, t.splits, g.splitk, g.err, g.st);
-  }
   if (N >= 256 && gemm_pairs_enabled() && e.mode != EPI_LOGITS && e.mode != EPI_DRELU2)
     return gemm_tc_launch<256, 2>(M, N, K, A, B, e, splits_for(256, 2), g.splitk, g.err, g.st);
   // one-CTA tiles: 256 wide (128 below 256 columns); fp32 outputs may take 192
@@ -618,6 +623,7 @@ static GemmEpilogue epi(int mode, void* C, long long ldc, int beta = 0, void* C2
   e.base_out = nullptr;
   e.vocab = e.col0 = 0;
   e.counter = nullptr;
+  e.n_run = 1;
   e.T = e.H = e.qk_norm = 0; e.eps = 0.f;
   return e;
 }

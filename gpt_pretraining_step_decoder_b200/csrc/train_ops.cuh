@@ -45,6 +45,19 @@ struct DeviceScope {
   TRY(scope_.enter(fn, p))
 #define CHECK_PTR(fn, p) TRY(scope_.check(fn, #p, p))
 
+// SMs of the device that p lies on (of the current one if p is no device memory,
+// which ON_DEVICE_OF then refuses): a call's tile forms and its workspace are planned
+// once, for the device that it will run on.
+static int sms_of(const void* p) {
+  cudaPointerAttributes a;
+  int sms = 0;
+  if (p && cudaPointerGetAttributes(&a, p) == cudaSuccess && a.type == cudaMemoryTypeDevice &&
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, a.device) == cudaSuccess)
+    return sms;
+  cudaGetLastError();
+  return device_sms();
+}
+
 // A strided block of rows in memory, for the checks that a call's outputs do not
 // overlap what it reads or writes elsewhere.
 struct Span {
@@ -150,8 +163,8 @@ extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long
 // 207 against 252).  A split adds its second launch and the partials' way
 // through L2; K is split in whole scale atoms (4 k-blocks).
 struct F8bPlan { int bn, cg, splits; };
-static F8bPlan f8b_plan(int M, int N, int K) {
-  const int quads = cdiv(K, 512), kb = cdiv(K, 128), sms = device_sms();
+static F8bPlan f8b_plan(int M, int N, int K, int sms) {
+  const int quads = cdiv(K, 512), kb = cdiv(K, 128);
   F8bPlan best{128, 1, 1};
   double best_t = 1e300;
   for (int cg = 1; cg <= (M > 128 && gemm_pairs_enabled() ? 2 : 1); ++cg)
@@ -190,7 +203,7 @@ static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda,
   TRY(make_tmap_gen(&p.tm_sfa, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sa, dsa, ls, bsa, CU_TENSOR_MAP_SWIZZLE_NONE));
   TRY(make_tmap_gen(&p.tm_sfb, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sb, dsb, ls, bsb, CU_TENSOR_MAP_SWIZZLE_NONE));
   p.a_atoms = cdiv(M, 128); p.b_atoms = cdiv(N, 128);
-  p.a_skip = 0; p.n_run = 1; p.k_chunk = 0;
+  p.a_skip = 0; p.k_chunk = 0;
   p.M = M; p.N = N; p.K = K; p.batch = 1;
   p.a_kmajor = 1; p.b_kmajor = 1;
   p.m_tiles = cdiv(M, CG * tc::BM);
@@ -224,7 +237,7 @@ static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda,
 extern "C" int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes) {
   if (!bytes || M < 1 || N < 1 || K < 1 || M > MAX_ROWS || N > MAX_ROWS || K > MAX_ROWS)
     return fail(GPT_ERR_ARG, "gptx_gemm_fp8_block_workspace_bytes: bad argument");
-  const F8bPlan pl = f8b_plan(M, N, K);
+  const F8bPlan pl = f8b_plan(M, N, K, device_sms());
   *bytes = pl.splits > 1 ? (size_t)pl.splits * M * N * 4 : 0;
   return GPT_OK;
 }
@@ -242,7 +255,7 @@ extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long l
       misaligned(C, 16) || misaligned(scales_a, 16) || misaligned(scales_b, 16))
     return fail(GPT_ERR_ARG, "%s: addresses and row pitches must be multiples of 16 bytes", fn);
   cudaStream_t st = (cudaStream_t)stream;
-  const F8bPlan pl = f8b_plan(M, N, K);
+  const F8bPlan pl = f8b_plan(M, N, K, sms_of(A));
   const size_t need = pl.splits > 1 ? (size_t)pl.splits * M * N * 4 : 0;
   if (need && (!workspace || ws_bytes < need))
     return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, need);
@@ -273,13 +286,13 @@ extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long l
 // tiles of the weight gradient (width x d) and of the logits (N x width) fill
 // whole waves of SM pairs over all pieces.  More pieces cost a pass over the
 // fp32 dx each, fewer cost memory.
-static int ce_piece(int N, int V, int d, int dtype, int asked) {
+static int ce_piece(int N, int V, int d, int dtype, int asked, int sms) {
   const int tiles = cdiv(V, 256);
   if (asked > 0) return std::min(V, 64 * cdiv(std::min(asked, V), 64));
   const long long budget = 512LL << 20, col_bytes = std::max(N, 1) * (long long)(dtype == GPT_DTYPE_BF16 ? 2 : 4) * 256;
   const int most = (int)std::max<long long>(1, std::min<long long>(tiles, budget / col_bytes));
   if (most >= tiles || dtype != GPT_DTYPE_BF16) return std::min(V, most * 256);
-  const int units = std::max(1, device_sms() / 2);
+  const int units = std::max(1, sms / 2);
   auto waves = [&](long long t) { return (double)((t + units - 1) / units); };
   int best = most;
   double best_cost = 1e300;
@@ -299,15 +312,17 @@ static int ce_piece(int N, int V, int d, int dtype, int asked) {
 struct CeWs {
   size_t stats, ztgt, part, counter, base, dz, dx, splitk, total;
   int piece, n_tiles;
+  TilePlan lse;  // bf16 forward: the product's form, which n_tiles follows
   long long splitk_elems;
 };
-static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked) {
+static CeWs ce_ws_plan(int N, int V, int d, int dtype, int backward, int asked, int sms) {
   CeWs w = {};
   Carver cv;
   const bool lp = dtype == GPT_DTYPE_BF16;
-  w.piece = ce_piece(N, V, d, dtype, asked);
+  w.piece = ce_piece(N, V, d, dtype, asked, sms);
   if (!backward) {
-    w.n_tiles = lp ? lse_pairs(N, V, d) : 1;
+    if (lp) w.lse = lse_plan(N, V, d, sms);
+    w.n_tiles = lp ? lse_pairs(V, w.lse) : 1;
     w.stats = cv.take((size_t)w.n_tiles * N * 8);
     w.ztgt = cv.take((size_t)N * 4);
     w.part = cv.take((size_t)cdiv(N, 32) * 16);
@@ -373,7 +388,7 @@ static int ce_check(const char* fn, const void* x, long long ldx, const void* w,
 extern "C" int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int vocab_piece, size_t* bytes) {
   if (!bytes || N < 0 || V < 1 || d < 1 || N > MAX_ROWS || V > MAX_ROWS || d > MAX_ROWS || vocab_piece < 0 || (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16))
     return fail(GPT_ERR_ARG, "linear_ce_workspace_bytes: bad argument");
-  *bytes = ce_ws_plan(N, V, d, dtype, backward != 0, vocab_piece).total;
+  *bytes = ce_ws_plan(N, V, d, dtype, backward != 0, vocab_piece, device_sms()).total;
   return GPT_OK;
 }
 
@@ -384,7 +399,7 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
   TRY(ce_check(fn, x, ldx, w, ldw, dtype, N, V, d, targets, softcap));
   if (!loss && !tok_loss && !lse) return fail(GPT_ERR_ARG, "%s: no output", fn);
   if (vocab_piece < 0) return fail(GPT_ERR_ARG, "%s: bad argument", fn);
-  const CeWs p = ce_ws_plan(N, V, d, dtype, 0, vocab_piece);
+  const CeWs p = ce_ws_plan(N, V, d, dtype, 0, vocab_piece, sms_of(workspace));
   if (!workspace || ws_bytes < p.total) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, p.total);
   if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
   const size_t fes = dtype_size(dtype);
@@ -406,11 +421,11 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
   float* ztgt = reinterpret_cast<float*>(b + p.ztgt);
   double2* part = reinterpret_cast<double2*>(b + p.part);
   unsigned* counter = reinterpret_cast<unsigned*>(b + p.counter);
-  const GemmCtx g{dtype == GPT_DTYPE_BF16, nullptr, 0, err, st, nullptr, true};
-  if (g.bf16) {
+  if (dtype == GPT_DTYPE_BF16) {
+    const GemmCtx g{true, nullptr, 0, err, st, nullptr};
     GemmEpilogue e = epi(EPI_LSE, nullptr, V);
     e.softcap = softcap; e.stats = stats; e.targets = targets; e.ztgt = ztgt; e.counter = counter;
-    TRY(gemm(g, N, V, d, op_k(x, ldx), op_k(w, ldw), e));
+    TRY(gemm_planned(g, p.lse, N, V, d, op_k(x, ldx), op_k(w, ldw), e));
   } else {
     float* z = reinterpret_cast<float*>(b + p.dz);
     for (int v0 = 0; v0 < V; v0 += p.piece) {
@@ -448,7 +463,8 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
              (dw && (misaligned(dw, 16) || (lddw * (long long)dtype_size(dw_dtype)) % 16))))
     return fail(GPT_ERR_ARG, "%s: gradient rows must be 16-byte aligned", fn);
   if (!lp && (misaligned(dx, 4) || misaligned(dw, 4))) return fail(GPT_ERR_ARG, "%s: a gradient is not aligned to its elements", fn);
-  const CeWs p = ce_ws_plan(N, V, d, dtype, 1, vocab_piece);
+  const int sms = sms_of(workspace);
+  const CeWs p = ce_ws_plan(N, V, d, dtype, 1, vocab_piece, sms);
   if (!workspace || ws_bytes < p.total) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, p.total);
   if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
   const size_t bes = dtype_size(dtype), wes = dtype_size(dw_dtype);
@@ -477,7 +493,7 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
     ++g_launches; launch_pdl(ce_base_kernel, 1, 1024, 0, st, scale, base);
     LAUNCH_CHECK();
   }
-  const GemmCtx g{lp, reinterpret_cast<float*>(b + p.splitk), p.splitk_elems, err, st, nullptr, true};
+  const GemmCtx g{true, reinterpret_cast<float*>(b + p.splitk), p.splitk_elems, err, st, nullptr};  // bf16
   const size_t es = dtype_size(dtype);
   void* dz = b + p.dz;
   const bool one = p.piece >= V;  // dx needs no sum over pieces
@@ -491,7 +507,7 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
       GemmEpilogue e = epi(EPI_DLOGITS, dz, ldz);
       e.softcap = softcap; e.targets = targets; e.vocab = V; e.col0 = v0; e.lse = lse; e.dtok = dtok; e.dloss = dloss;
       if (v0 == 0 && !count_aside) e.base_out = base;
-      TRY(gemm(g, N, width, d, op_k(x, ldx), op_k(wp, ldw), e));
+      TRY(gemm_planned(g, tile_plan(N, width, d, 0, sms), N, width, d, op_k(x, ldx), op_k(wp, ldw), e));
     } else {
       float* z = static_cast<float*>(dz);
       const float* xf = static_cast<const float*>(x);
@@ -508,13 +524,13 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
     if (dx) {
       GemmEpilogue e = one ? epi(EPI_STORE, dx, lddx) : epi(EPI_ACCUM_F32, acc, d, v0 > 0);
       if (one) e.scale_a = base;
-      TRY(gemm(g, N, d, width, op_k(dz, ldz), op_mn(wp, ldw), e, true));
+      TRY(gemm_planned(g, tile_plan(N, d, width, p.splitk_elems, sms), N, d, width, op_k(dz, ldz), op_mn(wp, ldw), e));
     }
     if (dw) {
       uint8_t* out = static_cast<uint8_t*>(dw) + (size_t)v0 * lddw * dtype_size(dw_dtype);
       GemmEpilogue e = dw_dtype == GPT_DTYPE_BF16 ? epi(EPI_STORE, out, lddw) : epi(EPI_ACCUM_F32, out, lddw, dw_beta);
       e.scale_a = base;
-      TRY(gemm(g, width, d, N, op_mn(dz, ldz), op_mn(x, ldx), e, true));
+      TRY(gemm_planned(g, tile_plan(width, d, N, p.splitk_elems, sms), width, d, N, op_mn(dz, ldz), op_mn(x, ldx), e));
     }
   }
   if (dx && lp && !one) {

@@ -462,7 +462,8 @@ int fp8_block_quantize(const void* x, int dtype, long long rows, long long cols,
                        long long ldq, uint8_t* scales, uint8_t* qt, long long ldqt, uint8_t* scales_t, void* stream);
 
 /* Device workspace bytes gptx_gemm_fp8_block() needs (0 when K is not split),
- * with the tile forms in force at the time (gptx_set_gemm_cta_pairs). */
+ * with the tile forms in force at the time (gptx_set_gemm_cta_pairs), on the
+ * device that is current (the call plans for its tensors' device). */
 int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes);
 
 /*
@@ -488,7 +489,8 @@ int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long long lda, co
  * linear_ce_backward() (backward != 0).  vocab_piece: columns of the vocabulary
  * taken at a time (0 = chosen, about 512 MB for N rows of them; the bf16
  * forward pass keeps no logits at all and takes none).  Pass the same value to
- * the call.  Counts the tile forms in force at the time (gptx_set_gemm_cta_pairs).
+ * the call.  Counts the tile forms in force at the time (gptx_set_gemm_cta_pairs),
+ * on the device that is current (the call plans for its tensors' device).
  */
 int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int vocab_piece, size_t* bytes);
 

@@ -1,0 +1,72 @@
+"""Calls of the standalone training operators at the edges of what their
+documentation allows."""
+
+import threading
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def g():
+    import torch
+    import gpt_pretraining_step_decoder_b200 as g
+    assert torch.cuda.is_available()
+    return g
+
+
+def ce_inputs(N, V, d, seed=0, spread=2.0):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(N, d, generator=gen, device="cuda").bfloat16()
+    w = (torch.randn(V, d, generator=gen, device="cuda") * spread / d ** 0.5).bfloat16()
+    t = torch.randint(0, V, (N,), generator=gen, device="cuda", dtype=torch.int32)
+    return x, w, t
+
+
+def ce_forward(g, x, w, t, softcap=0.0, ws=None):
+    import torch
+    (N, d), V = x.shape, w.shape[0]
+    code = g.DTYPE_BF16 if x.dtype == torch.bfloat16 else g.DTYPE_F32
+    if ws is None:
+        ws = torch.empty(g.linear_ce_workspace_bytes(N, V, d, code, 0), dtype=torch.uint8, device="cuda")
+    loss, tok, lse = (torch.empty(k, device="cuda") for k in (1, N, N))
+    g.linear_ce_forward(x, d, w, d, code, N, V, d, t, softcap, loss, tok, lse, ws, ws.numel())
+    torch.cuda.synchronize()
+    return loss, tok, lse
+
+
+def test_tile_forms_switched_during_calls(g):
+    """A thread that switches the GEMMs' tile forms while another one forms losses:
+    each loss is that of one form or the other (the number of statistics that the
+    product writes is the number that the workspace and the joining kernel count on)."""
+    import torch
+    N, V, d = 300, 16384, 768
+    x, w, t = ce_inputs(N, V, d)
+    want, sizes = [], []
+    for on in (False, True):
+        g.gptx_set_gemm_cta_pairs(on)
+        sizes.append(g.linear_ce_workspace_bytes(N, V, d, g.DTYPE_BF16, 0))
+        want.append(ce_forward(g, x, w, t))
+    assert sizes[0] != sizes[1]                       # the forms leave different numbers of statistics
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
+    stop = threading.Event()
+
+    def switch():
+        while not stop.is_set():
+            for on in (0, 1):
+                g._lib.gptx_set_gemm_cta_pairs(on)
+
+    th = threading.Thread(target=switch)
+    th.start()
+    try:
+        for _ in range(1500):
+            got = ce_forward(g, x, w, t, ws=ws)
+            assert any(all(torch.equal(a, b) for a, b in zip(got, ref)) for ref in want)
+    finally:
+        stop.set()
+        th.join()
+        g.gptx_set_gemm_cta_pairs(True)
+    assert g.ngram_sync_status() == g.GPT_OK
