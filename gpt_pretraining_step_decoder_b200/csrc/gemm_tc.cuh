@@ -1061,6 +1061,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (mj != -INFINITY) {
             rsum = rsum * __expf(rmax - mj) + run_sum * __expf(run_max - mj);
             rmax = mj;
+          } else {
+            rsum += run_sum;  // no maximum so far: sums of 0, or a NaN, which stays
           }
         }
         run_max = rmax;

@@ -70,3 +70,23 @@ def test_tile_forms_switched_during_calls(g):
         th.join()
         g.gptx_set_gemm_cta_pairs(True)
     assert g.ngram_sync_status() == g.GPT_OK
+
+
+@pytest.mark.parametrize("softcap", [0.0, 15.0, 100.0])
+@pytest.mark.parametrize("N,V,d,rows", [
+    (33, 50112, 768, (49984, 50048)),     # one row block: runs of three 128-column tiles, the last run of two
+    (33, 50048, 64, (49792, 49920)),      # runs of two 256-column tiles
+    (16384, 50560, 64, (50304, 50432)),   # pairs, runs of four 256-column tiles, the last run of two
+])
+def test_nan_rows_of_the_weight_before_an_empty_half_tile(g, N, V, d, rows, softcap):
+    """NaN in the classes of a whole half tile whose neighbour in the run lies past
+    the vocabulary: the row's sum is NaN, and the loss is reported as not finite."""
+    import torch
+    x, w, t = ce_inputs(N, V, d)
+    t.clamp_(max=rows[0] - 1)
+    loss, _, lse = ce_forward(g, x, w, t, softcap)
+    assert torch.isfinite(lse).all() and g.ngram_sync_status() == g.GPT_OK
+    w[rows[0]:rows[1]] = float("nan")
+    loss, _, lse = ce_forward(g, x, w, t, softcap)
+    assert torch.isnan(lse).all() and torch.isnan(loss).all()
+    assert g.ngram_sync_status() == g.GPT_ERR_NONFINITE
