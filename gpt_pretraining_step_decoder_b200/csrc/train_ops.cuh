@@ -399,6 +399,8 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
   TRY(ce_check(fn, x, ldx, w, ldw, dtype, N, V, d, targets, softcap));
   if (!loss && !tok_loss && !lse) return fail(GPT_ERR_ARG, "%s: no output", fn);
   if (vocab_piece < 0) return fail(GPT_ERR_ARG, "%s: bad argument", fn);
+  if (misaligned(loss, 4) || misaligned(tok_loss, 4) || misaligned(lse, 4))
+    return fail(GPT_ERR_ARG, "%s: an output is not aligned to its elements", fn);
   const CeWs p = ce_ws_plan(N, V, d, dtype, 0, vocab_piece, sms_of(workspace));
   if (!workspace || ws_bytes < p.total) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, p.total);
   if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
@@ -463,6 +465,8 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
              (dw && (misaligned(dw, 16) || (lddw * (long long)dtype_size(dw_dtype)) % 16))))
     return fail(GPT_ERR_ARG, "%s: gradient rows must be 16-byte aligned", fn);
   if (!lp && (misaligned(dx, 4) || misaligned(dw, 4))) return fail(GPT_ERR_ARG, "%s: a gradient is not aligned to its elements", fn);
+  if (misaligned(lse, 4) || misaligned(dloss, 4) || misaligned(dtok, 4))
+    return fail(GPT_ERR_ARG, "%s: lse, dloss or dtok is not aligned to its elements", fn);
   const int sms = sms_of(workspace);
   const CeWs p = ce_ws_plan(N, V, d, dtype, 1, vocab_piece, sms);
   if (!workspace || ws_bytes < p.total) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, p.total);
@@ -644,6 +648,7 @@ extern "C" int grad_clip(int n, const void* const* grads, void* const* outs, con
     if (sizes[i] > 0 && (misaligned(grads[i], es) || (outs && misaligned(outs[i], es))))
       return fail(GPT_ERR_ARG, "%s: tensor %d is not aligned to its elements", fn, i);
   }
+  if (misaligned(norm_out, 4)) return fail(GPT_ERR_ARG, "%s: norm_out is not aligned to its elements", fn);
   if (!workspace || ws_bytes < need) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, need);
   if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
   if (n > 0) {

@@ -1,0 +1,45 @@
+"""More argument checks of the standalone training operators, made on the host
+before any device work (no GPU needed).  Addresses are stand-ins that are never
+dereferenced; a call that passes the checks goes on to the device, which this
+machine may not have, and ends with another status."""
+
+import ctypes
+
+import pytest
+
+import gpt_pretraining_step_decoder_b200 as g
+
+A, B, C, D, E, F, WS = (i << 24 for i in range(1, 8))
+
+
+def ce_forward(loss=D, tok=E, lse=F, **kw):
+    a = dict(x=A, ldx=64, w=B, ldw=64, dtype=g.DTYPE_BF16, N=10, V=100, d=64, t=C, cap=0.0)
+    a.update(kw)
+    return g._lib.linear_ce_forward(*a.values(), loss, tok, lse, 0, WS, 1 << 30, None)
+
+
+def ce_backward(lse=D, dloss=None, dtok=None, dx=E, dw=F, **kw):
+    a = dict(x=A, ldx=64, w=B, ldw=64, dtype=g.DTYPE_BF16, N=10, V=100, d=64, t=C, cap=0.0)
+    a.update(kw)
+    return g._lib.linear_ce_backward(*a.values(), lse, dloss, dtok, dx, 64, dw, 64, a["dtype"], 0, 0, WS, 1 << 30, None)
+
+
+def clip(grads, sizes, dtypes=None, outs=None, max_norm=1.0, norm=None, ws=WS, ws_bytes=1 << 20):
+    n = len(grads)
+    P, L, I = ctypes.c_void_p * n, ctypes.c_longlong * n, ctypes.c_int * n
+    return g._lib.grad_clip(n, P(*grads), None if outs is None else P(*outs), L(*sizes), I(*(dtypes or [0] * n)),
+                            max_norm, norm, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("dtype", [g.DTYPE_BF16, g.DTYPE_F32])
+@pytest.mark.parametrize("off", [1, 2])
+def test_fp32_vectors_off_their_alignment(dtype, off):
+    """Every float that a kernel reads or writes has to lie on 4 bytes."""
+    for bad in (dict(loss=D + off), dict(tok=E + off), dict(lse=F + off)):
+        assert ce_forward(dtype=dtype, **bad) == g.GPT_ERR_ARG
+        assert "aligned" in g.gpt_last_error()
+    for bad in (dict(lse=D + off), dict(dloss=D + 4096 + off), dict(dtok=D + 4096 + off)):
+        assert ce_backward(dtype=dtype, **bad) == g.GPT_ERR_ARG
+        assert "aligned" in g.gpt_last_error()
+    assert clip([A], [3], norm=D + off) == g.GPT_ERR_ARG
+    assert "aligned" in g.gpt_last_error()
