@@ -651,6 +651,16 @@ extern "C" int grad_clip(int n, const void* const* grads, void* const* outs, con
   if (misaligned(norm_out, 4)) return fail(GPT_ERR_ARG, "%s: norm_out is not aligned to its elements", fn);
   if (!workspace || ws_bytes < need) return fail(GPT_ERR_WORKSPACE, "%s: needs %zu bytes of workspace", fn, need);
   if (misaligned(workspace, 256)) return fail(GPT_ERR_ARG, "workspace not 256-byte aligned");
+  // blocks still read the partials while one writes the norm, and the tensors while
+  // others write partials: both lie apart from everything else
+  const Span own[] = {{"the workspace", workspace, 1, need, 0}, {"norm_out", norm_out, 1, 4, 0}};
+  TRY(check_spans(fn, own, 1, 2));
+  for (int i = 0; i < n; ++i)
+    for (const void* p : {grads[i], outs ? static_cast<const void*>(outs[i]) : nullptr}) {
+      const Span t{"a tensor", sizes[i] > 0 ? p : nullptr, 1, (unsigned long long)sizes[i] * dtype_size(dtypes[i]), 0};
+      for (const Span& o : own)
+        if (spans_overlap(o, t)) return fail(GPT_ERR_ARG, "%s: tensor %d overlaps %s", fn, i, o.name);
+    }
   if (n > 0) {
     int* order = static_cast<int*>(malloc((size_t)n * sizeof(int)));
     if (!order) return fail(GPT_ERR_ARG, "%s: out of host memory", fn);

@@ -548,7 +548,8 @@ int grad_clip_workspace_bytes(int n, size_t* bytes);
  * counts (0 allowed) and GPT_DTYPE_F32 / GPT_DTYPE_BF16, read before the call
  * returns.  outs = null clips in place (and writes nothing when coef is 1);
  * otherwise outs[i] has grads[i]'s type and size.  An output must not
- * overlap another output or another tensor's input (refused).  Any element-aligned address (16 bytes
+ * overlap another output or another tensor's input; the workspace and norm_out
+ * must not overlap a tensor or each other (refused).  Any element-aligned address (16 bytes
  * are faster).  max_norm = 0: no scaling.  The squares are summed in fp64
  * in a fixed order (bit-reproducible); a norm that is not finite leaves the
  * gradients unscaled and is reported as GPT_ERR_NONFINITE by the next

@@ -43,3 +43,23 @@ def test_fp32_vectors_off_their_alignment(dtype, off):
         assert "aligned" in g.gpt_last_error()
     assert clip([A], [3], norm=D + off) == g.GPT_ERR_ARG
     assert "aligned" in g.gpt_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(grads=[A], sizes=[4], norm=WS), dict(grads=[A], sizes=[4], norm=WS + 1024), dict(grads=[], sizes=[], norm=WS + 8),
+    dict(grads=[A], sizes=[4], norm=A + 12), dict(grads=[A], sizes=[4], outs=[B], norm=A),
+    dict(grads=[A], sizes=[4], outs=[B], norm=B + 4), dict(grads=[A, WS - 8], sizes=[4, 4]),
+    dict(grads=[A, WS + 512], sizes=[4, 4], dtypes=[0, 1]), dict(grads=[A, B], sizes=[4, 1 << 25], outs=[C, F - 512]),
+])
+def test_clip_norm_and_workspace_lie_apart(kw):
+    """The norm is written while the partials and the tensors are still read."""
+    assert clip(**kw) == g.GPT_ERR_ARG
+    assert "overlaps" in g.gpt_last_error()
+
+
+def test_clip_neighbours_of_norm_and_workspace_pass():
+    need = g.grad_clip_workspace_bytes(1)
+    for kw in (dict(grads=[A], sizes=[4], norm=A + 16), dict(grads=[A], sizes=[4], norm=A - 4),
+               dict(grads=[WS - 16], sizes=[4], norm=WS + need), dict(grads=[WS + 8], sizes=[0])):
+        clip(**kw)
+        assert "overlaps" not in g.gpt_last_error()
