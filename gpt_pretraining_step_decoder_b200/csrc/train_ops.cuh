@@ -661,7 +661,7 @@ extern "C" int grad_clip(int n, const void* const* grads, void* const* outs, con
       for (const Span& o : own)
         if (spans_overlap(o, t)) return fail(GPT_ERR_ARG, "%s: tensor %d overlaps %s", fn, i, o.name);
     }
-  if (n > 0) {
+  if (n > 0 && (outs || max_norm > 0.f)) {  // a norm alone writes no tensor
     int* order = static_cast<int*>(malloc((size_t)n * sizeof(int)));
     if (!order) return fail(GPT_ERR_ARG, "%s: out of host memory", fn);
     const int bad = clip_overlap(n, grads, outs, sizes, dtypes, order);

@@ -550,7 +550,8 @@ int grad_clip_workspace_bytes(int n, size_t* bytes);
  * otherwise outs[i] has grads[i]'s type and size.  An output must not
  * overlap another output or another tensor's input; the workspace and norm_out
  * must not overlap a tensor or each other (refused).  Any element-aligned address (16 bytes
- * are faster).  max_norm = 0: no scaling.  The squares are summed in fp64
+ * are faster).  max_norm = 0: no scaling (with outs =
+ * null the norm alone, of tensors that may then share memory).  The squares are summed in fp64
  * in a fixed order (bit-reproducible); a norm that is not finite leaves the
  * gradients unscaled and is reported as GPT_ERR_NONFINITE by the next
  * ngram_sync_status().  norm_out: device float, nullable.  workspace: device, 256-byte

@@ -90,3 +90,13 @@ def test_nan_rows_of_the_weight_before_an_empty_half_tile(g, N, V, d, rows, soft
     loss, _, lse = ce_forward(g, x, w, t, softcap)
     assert torch.isnan(lse).all() and torch.isnan(loss).all()
     assert g.ngram_sync_status() == g.GPT_ERR_NONFINITE
+
+
+def test_norm_alone_counts_a_shared_tensor_each_time(g):
+    import torch
+    t = torch.randn(1000, device="cuda")
+    ws = torch.empty(g.grad_clip_workspace_bytes(3), dtype=torch.uint8, device="cuda")
+    norm, keep = torch.zeros(1, device="cuda"), t.clone()
+    g.grad_clip([t, t, t[100:]], None, 0.0, norm, ws, ws.numel())
+    want = (2 * t.double().square().sum() + t[100:].double().square().sum()).sqrt().item()
+    assert abs(norm.item() - want) <= 2.0 ** -23 * want and torch.equal(t, keep)

@@ -63,3 +63,12 @@ def test_clip_neighbours_of_norm_and_workspace_pass():
                dict(grads=[WS - 16], sizes=[4], norm=WS + need), dict(grads=[WS + 8], sizes=[0])):
         clip(**kw)
         assert "overlaps" not in g.gpt_last_error()
+
+
+def test_norm_alone_of_tensors_that_share_memory():
+    """max_norm = 0 in place writes no tensor: a weight listed twice is no overlap."""
+    for kw in (dict(grads=[A, A], sizes=[4, 4]), dict(grads=[A, A + 8, A], sizes=[4, 4, 1])):
+        clip(max_norm=0.0, **kw)
+        assert "overlaps" not in g.gpt_last_error()
+        assert clip(max_norm=1.0, **kw) == g.GPT_ERR_ARG
+        assert clip(max_norm=0.0, outs=[B + 64 * i for i in range(len(kw["grads"]) - 1)] + [A], **kw) == g.GPT_ERR_ARG
