@@ -414,12 +414,13 @@ _clip_codes = None  # torch element type -> DTYPE_*
 
 
 def grad_clip(grads, outs, max_norm, norm_out, workspace, ws_bytes, stream=None):
-    """Global L2 norm of a list of contiguous fp32 / bf16 CUDA tensors into
+    """Global L2 norm of contiguous fp32 / bf16 CUDA tensors (any iterable) into
     norm_out (device float, or None), and the tensors scaled by min(1, max_norm /
     (norm + 1e-6)): in place (outs None) or into the tensors of outs, which
     have the same sizes and types.  max_norm = 0: no scaling."""
     import torch
     T = torch.Tensor
+    grads, outs = list(grads), None if outs is None else list(outs)  # each is gone through several times
     global _clip_codes
     if _clip_codes is None:
         _clip_codes = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}

@@ -100,3 +100,14 @@ def test_norm_alone_counts_a_shared_tensor_each_time(g):
     g.grad_clip([t, t, t[100:]], None, 0.0, norm, ws, ws.numel())
     want = (2 * t.double().square().sum() + t[100:].double().square().sum()).sqrt().item()
     assert abs(norm.item() - want) <= 2.0 ** -23 * want and torch.equal(t, keep)
+
+
+def test_clip_of_an_iterator_of_tensors(g):
+    import torch
+    grads = [torch.randn(n, device="cuda") for n in (300, 7)]
+    ws = torch.empty(g.grad_clip_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+    norm = torch.zeros(1, device="cuda")
+    want = sum(t.double().square().sum() for t in grads).sqrt().item()
+    g.grad_clip((t for t in grads), None, 0.5, norm, ws, ws.numel())
+    after = sum(t.double().square().sum() for t in grads).sqrt().item()
+    assert abs(norm.item() - want) <= 2.0 ** -23 * want and abs(after - 0.5) <= 1e-6

@@ -72,3 +72,15 @@ def test_norm_alone_of_tensors_that_share_memory():
         assert "overlaps" not in g.gpt_last_error()
         assert clip(max_norm=1.0, **kw) == g.GPT_ERR_ARG
         assert clip(max_norm=0.0, outs=[B + 64 * i for i in range(len(kw["grads"]) - 1)] + [A], **kw) == g.GPT_ERR_ARG
+
+
+def test_clip_of_an_iterator_of_tensors():
+    """A generator's tensors all reach the call (the same one twice is refused there)."""
+    import torch
+    t, u = torch.zeros(4), torch.zeros(4)
+    for grads, outs in (((x for x in (t, t)), None), (iter([t, u]), (x for x in (t, t)))):
+        with pytest.raises(g.GptError) as e:
+            g.grad_clip(grads, outs, 1.0, None, WS, 1 << 20)
+        assert e.value.code == g.GPT_ERR_ARG and "overlaps" in str(e.value)
+    with pytest.raises(ValueError):
+        g.grad_clip((x for x in (t, u)), (x for x in (t,)), 1.0, None, WS, 1 << 20)
