@@ -124,16 +124,17 @@ extern "C" int fp8_block_quantize(const void* x, int dtype, long long rows, long
                                   uint8_t* q, long long ldq, uint8_t* scales, uint8_t* qt, long long ldqt,
                                   uint8_t* scales_t, void* stream) {
   const char* fn = "fp8_block_quantize";
-  if (!x || rows < 0 || cols < 0 || rows > MAX_ROWS || cols > MAX_ROWS || ldx < cols || (!q && !qt))
+  if (rows < 0 || cols < 0 || rows > MAX_ROWS || cols > MAX_ROWS || ldx < cols)
     return fail(GPT_ERR_ARG, "%s: bad argument", fn);
   if (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16) return fail(GPT_ERR_ARG, "%s: bad dtype", fn);
+  if (rows == 0 || cols == 0) return GPT_OK;  // whatever the addresses: an empty tensor has none
+  if (!x || (!q && !qt)) return fail(GPT_ERR_ARG, "%s: bad argument", fn);
   if ((q && (!scales || ldq < cols || ldq % 16 || misaligned(q, 16) || misaligned(scales, 16))) ||
       (qt && (!scales_t || ldqt < rows || ldqt % 16 || misaligned(qt, 16) || misaligned(scales_t, 16))))
     return fail(GPT_ERR_ARG, "%s: codes need scales, a row pitch that covers a row in a multiple of 16 bytes, "
                              "and 16-byte aligned addresses", fn);
   if (misaligned(x, dtype_size(dtype))) return fail(GPT_ERR_ARG, "%s: x is not aligned to its elements", fn);
   const long long tiles = cdiv_ll(rows, 128) * cdiv_ll(cols, 128);
-  if (tiles == 0) return GPT_OK;
   const unsigned long long sb = scale_atoms(rows, cols) * 512, sbt = scale_atoms(cols, rows) * 512;
   const Span spans[] = {{"q", q, rows, (unsigned long long)cols, (unsigned long long)ldq}, {"scales", q ? scales : nullptr, 1, sb, 0},
                         {"qt", qt, cols, (unsigned long long)rows, (unsigned long long)ldqt},
@@ -397,7 +398,7 @@ extern "C" int linear_ce_forward(const void* x, long long ldx, const void* w, lo
                                  int vocab_piece, void* workspace, size_t ws_bytes, void* stream) {
   const char* fn = "linear_ce_forward";
   TRY(ce_check(fn, x, ldx, w, ldw, dtype, N, V, d, targets, softcap));
-  if (!loss && !tok_loss && !lse) return fail(GPT_ERR_ARG, "%s: no output", fn);
+  if (N > 0 && !loss && !tok_loss && !lse) return fail(GPT_ERR_ARG, "%s: no output", fn);
   if (vocab_piece < 0) return fail(GPT_ERR_ARG, "%s: bad argument", fn);
   if (misaligned(loss, 4) || misaligned(tok_loss, 4) || misaligned(lse, 4))
     return fail(GPT_ERR_ARG, "%s: an output is not aligned to its elements", fn);
@@ -456,7 +457,7 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
   const char* fn = "linear_ce_backward";
   TRY(ce_check(fn, x, ldx, w, ldw, dtype, N, V, d, targets, softcap));
   const bool lp = dtype == GPT_DTYPE_BF16;
-  if ((N > 0 && !lse) || (!dx && !dw) || (dx && lddx < d) || (dw && lddw < d) || (dloss && dtok) || vocab_piece < 0)
+  if ((N > 0 && (!lse || (!dx && !dw))) || (dx && lddx < d) || (dw && lddw < d) || (dloss && dtok) || vocab_piece < 0)
     return fail(GPT_ERR_ARG, "%s: bad argument", fn);
   if (dw && ((dw_dtype != GPT_DTYPE_F32 && dw_dtype != GPT_DTYPE_BF16) || (!lp && dw_dtype != GPT_DTYPE_F32) ||
              (dw_beta && dw_dtype != GPT_DTYPE_F32)))

@@ -453,7 +453,8 @@ int fp8_block_scale_bytes(long long rows, long long cols, size_t* bytes);
  * row pitch ldq bytes, with `scales`; qt: device uint8 [cols, rows], pitch ldqt, the
  * codes of the transpose with scales_t, its groups running along x's rows; either
  * of q and qt may be null, x is read once for both.  Code addresses and pitches
- * are multiples of 16 bytes; bytes between cols and ldq are left as they are.
+ * are multiples of 16 bytes; bytes between cols and ldq are left as they are.  No rows
+ * or no columns: nothing is done, and addresses may be null.
  * The forward product of a linear layer takes x (square = 0) and W (square = 1);
  * its data gradient dY and the transposed W; its weight gradient the transposed dY
  * and the transposed x.  Asynchronous on `stream`.
@@ -468,7 +469,7 @@ int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes);
 
 /*
  * C[m, n] = (beta ? C[m, n] : 0) + sum_k A[m, k] B[n, k] with A [M, K] and
- * B [N, K] codes and scales as fp8_block_quantize leaves them, on the tcgen05
+ * B [N, K] (M, N, K >= 1) codes and scales as fp8_block_quantize leaves them, on the tcgen05
  * tensor cores, which apply the scales (kind::mxf8f6f4.block_scale, fp32
  * accumulation; SM pairs when gptx_set_gemm_cta_pairs is on).  lda, ldb: row
  * pitches of the codes in bytes; what lies between K and the pitch is not read.
@@ -508,7 +509,8 @@ int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int 
  * float, each nullable; keep lse for the backward pass.  The logits are formed
  * in tiles on the tensor cores with fp32 accumulation and reduced there (fp32 mode:
  * FFMA, a piece of fp32 logits at a time in the workspace); sums are formed
- * in a fixed order.  N = 0 gives a loss of 0.  workspace: 256-byte aligned.
+ * in a fixed order.  N = 0 gives a loss of 0; the addresses of its [0]-sized tensors may
+ * be null, here and in the backward pass (which leaves dW = 0, or as it was with dw_beta).  workspace: 256-byte aligned.
  * Asynchronous on `stream`.
  */
 int linear_ce_forward(const void* x, long long ldx, const void* w, long long ldw, int dtype, int N, int V, int d,

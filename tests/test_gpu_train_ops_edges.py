@@ -111,3 +111,21 @@ def test_clip_of_an_iterator_of_tensors(g):
     g.grad_clip((t for t in grads), None, 0.5, norm, ws, ws.numel())
     after = sum(t.double().square().sum() for t in grads).sqrt().item()
     assert abs(norm.item() - want) <= 2.0 ** -23 * want and abs(after - 0.5) <= 1e-6
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_empty_batch(g, dtype):
+    """A batch of no tokens through quantizer, loss and gradient, as a program's empty
+    tensors arrive (their addresses are null)."""
+    import torch
+    dt, code = (torch.bfloat16, g.DTYPE_BF16) if dtype == "bf16" else (torch.float32, g.DTYPE_F32)
+    new = lambda *s, dt=dt: torch.empty(*s, dtype=dt, device="cuda")  # noqa: E731
+    x, t, tok, dx = new(0, 64), new(0, dt=torch.int32), new(0, dt=torch.float32), new(0, 64)
+    w = torch.randn(200, 64, device="cuda").to(dt)
+    q, sc = new(0, 64, dt=torch.uint8), new(0, dt=torch.uint8)
+    g.fp8_block_quantize(x, code, 0, 64, 64, False, q, 64, sc)
+    ws = new(g.linear_ce_workspace_bytes(0, 200, 64, code, 1), dt=torch.uint8)
+    g.linear_ce_forward(x, 64, w, 64, code, 0, 200, 64, t, 0.0, None, tok, tok, ws, ws.numel())
+    g.linear_ce_backward(x, 64, w, 64, code, 0, 200, 64, t, 0.0, tok, None, None, dx, 64, None, 64, code, 0, ws, ws.numel())
+    torch.cuda.synchronize()
+    assert g.ngram_sync_status() == g.GPT_OK

@@ -84,3 +84,22 @@ def test_clip_of_an_iterator_of_tensors():
         assert e.value.code == g.GPT_ERR_ARG and "overlaps" in str(e.value)
     with pytest.raises(ValueError):
         g.grad_clip((x for x in (t, u)), (x for x in (t,)), 1.0, None, WS, 1 << 20)
+
+
+@pytest.mark.parametrize("rows,cols", [(0, 100), (5, 0), (0, 0)])
+@pytest.mark.parametrize("dtype", [g.DTYPE_BF16, g.DTYPE_F32])
+def test_quantize_of_an_empty_tensor(rows, cols, dtype):
+    """An empty tensor's address is null: still no call, in either orientation."""
+    assert g._lib.fp8_block_quantize(None, dtype, rows, cols, cols, 0, None, 0, None, None, 0, None, None) == g.GPT_OK
+    assert g._lib.fp8_block_quantize(None, dtype, rows, cols, cols, 1, None, 112, C, D, 0, None, None) == g.GPT_OK
+    assert g._lib.fp8_block_quantize(None, 2, rows, cols, cols, 0, None, 0, None, None, 0, None, None) == g.GPT_ERR_ARG
+    assert g._lib.fp8_block_quantize(None, dtype, -1, cols, cols, 0, None, 0, None, None, 0, None, None) == g.GPT_ERR_ARG
+
+
+def test_ce_of_no_rows_with_empty_outputs():
+    """N = 0: per-token outputs and dx are empty, their addresses null; the call passes the checks."""
+    for st in (ce_forward(N=0, x=None, t=None, loss=None, tok=None, lse=None),
+               ce_backward(N=0, x=None, t=None, lse=None, dx=None, dw=None)):
+        assert st != g.GPT_ERR_ARG or "device" in g.gpt_last_error()
+    assert ce_forward(loss=None, tok=None, lse=None) == g.GPT_ERR_ARG
+    assert ce_backward(dx=None, dw=None) == g.GPT_ERR_ARG
