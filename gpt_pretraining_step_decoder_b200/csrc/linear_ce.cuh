@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(32 * G) ce_combine_kernel(const float2* __rest
 }
 
 // fp32: gradient scale of a row: dtok[i], or base = dloss / count (dloss null: 1),
-// 0 for ignored rows.  Every block counts the targets itself (they are in L2), so
-// that no launch has to come first.
+// 0 for ignored rows.  With few rows every block counts the targets itself (they are
+// in L2), so that no launch has to come first; for more ce_base_kernel counts them once.
 struct CeRowScale {
   const int32_t* targets;
   const float* dloss;
@@ -158,7 +158,7 @@ __device__ __forceinline__ float ce_row_scale(const CeRowScale& a, float base, i
   if (y < -1 || y >= a.V) set_error(a.err, GPT_EBIT_INPUT);
   return y >= 0 && y < a.V ? (a.dtok ? a.dtok[i] : base) : 0.f;
 }
-// base alone, for more rows than the first CTA of the bf16 product counts on the side
+// base alone, for more rows than the first product counts on the side
 __global__ void __launch_bounds__(1024) ce_base_kernel(const CeRowScale a, float* __restrict__ base) {
   pdl_wait();
   const float b = ce_scale_base(a);
@@ -225,6 +225,7 @@ struct CeProduct {
 struct CeGrad {
   const float* lse;
   CeRowScale scale;
+  const float* base;  // counted before (null: by every block)
   int col0;
   float softcap;
   unsigned* zero;  // CEP_TILES counters to zero for the next launch (null: none)
@@ -295,7 +296,8 @@ __global__ void __launch_bounds__(CEP_WARPS * 32, 2) ce_product_kernel(const CeP
   }
   if (gr.zero && blockIdx.x == 0)
     for (int i = threadIdx.x; i < CEP_TILES; i += CEP_WARPS * 32) gr.zero[i] = 0u;
-  const float base = grad ? ce_scale_base(gr.scale) : 0.f;  // while the first chunk is on its way
+  // while the first chunk is on its way
+  const float base = !grad ? 0.f : gr.base ? *gr.base : ce_scale_base(gr.scale);
   for (; k0 < k1; k0 += STEP) {
     __syncwarp();
     ce_store_chunk(as, va, p.a_kmajor);

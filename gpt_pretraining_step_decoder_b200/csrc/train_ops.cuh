@@ -309,6 +309,13 @@ static int ce_piece(int N, int V, int d, int dtype, int asked, int sms) {
   return std::min(V, best * 256);
 }
 
+// More rows than these: the targets are counted by a launch of their own instead of
+// inside the gradient's first product.  There bf16 counts them in one CTA, beside its
+// first tile; fp32 in every block, which costs N^2 V / 1024 reads (B200, a launch
+// aside against in every block: 600 x 4096 x 64 61.0 and 63.7 us, 4096 x 4096 x 64 344 and
+// 377, 65536 x 4096 x 16 4.0 and 12.2 ms).
+constexpr int CE_COUNT_ROWS_BF16 = 4096, CE_COUNT_ROWS_F32 = 512;
+
 // Byte offsets of the operator's scratch inside the caller's workspace.
 struct CeWs {
   size_t stats, ztgt, part, counter, base, dz, dx, splitk, total;
@@ -491,10 +498,10 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
   uint8_t* b = static_cast<uint8_t*>(workspace);
   const CeRowScale scale{targets, dloss, dtok, N, V, err};
   unsigned* counter = reinterpret_cast<unsigned*>(b + p.counter);
-  // the mean's factor, applied by the products (bf16); per-token gradients go into dz
+  // the mean's factor: applied by the products in bf16, to dz in fp32 (as per-token gradients are in both)
   float* base = dtok ? nullptr : reinterpret_cast<float*>(b + p.base);
-  const bool count_aside = N > 4096;
-  if (lp && base && count_aside) {
+  const bool count_aside = N > (lp ? CE_COUNT_ROWS_BF16 : CE_COUNT_ROWS_F32);
+  if (base && count_aside) {
     ++g_launches; launch_pdl(ce_base_kernel, 1, 1024, 0, st, scale, base);
     LAUNCH_CHECK();
   }
@@ -518,7 +525,7 @@ extern "C" int linear_ce_backward(const void* x, long long ldx, const void* w, l
       const float* xf = static_cast<const float*>(x);
       const float* wf = reinterpret_cast<const float*>(wp);
       TRY(ce_products(ce_product(xf, ldx, 1, wf, ldw, 1, z, width, N, width, d, 0), CeProduct{},
-                      CeGrad{lse, scale, v0, softcap, counter}, st));
+                      CeGrad{lse, scale, count_aside ? base : nullptr, v0, softcap, counter}, st));
       CeProduct px = ce_no_product, pw = ce_no_product;
       if (dx) px = ce_product(z, width, 1, wf, ldw, 0, acc, lddx, N, d, width, v0 > 0);
       if (dw) pw = ce_product(z, width, 0, xf, ldx, 0, static_cast<float*>(dw) + v0 * lddw, lddw, width, d, N, dw_beta);

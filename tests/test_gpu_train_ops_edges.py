@@ -129,3 +129,41 @@ def test_empty_batch(g, dtype):
     g.linear_ce_backward(x, 64, w, 64, code, 0, 200, 64, t, 0.0, tok, None, None, dx, 64, None, 64, code, 0, ws, ws.numel())
     torch.cuda.synchronize()
     assert g.ngram_sync_status() == g.GPT_OK
+
+
+def device_ms(call, n=3):
+    import torch
+    call()
+    times = []
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times)
+
+
+def test_counting_the_targets_does_not_grow_with_the_product(g):
+    """fp32, many rows and a small width: the gradient of the mean costs what that of
+    per-token losses does, which has no targets to count (three times as much where
+    every block of the product counted all of them)."""
+    import torch
+    N, V, d = 65536, 4096, 16
+    x, w = torch.randn(N, d, device="cuda"), torch.randn(V, d, device="cuda") / 4
+    t = torch.randint(-1, V, (N,), device="cuda", dtype=torch.int32)
+    lse = ce_forward(g, x, w, t)[2]
+    n = g.linear_ce_workspace_bytes(N, V, d, g.DTYPE_F32, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dtok = torch.full((N,), 1.0, device="cuda") / (t >= 0).sum()
+    grads = [(torch.empty_like(x), torch.empty_like(w)) for _ in range(2)]
+
+    def backward(dtok, dx, dw):
+        g.linear_ce_backward(x, d, w, d, g.DTYPE_F32, N, V, d, t, 0.0, lse, None, dtok, dx, d, dw, d, g.DTYPE_F32, 0, ws, n)
+
+    mean = device_ms(lambda: backward(None, *grads[0]))
+    tokens = device_ms(lambda: backward(dtok, *grads[1]))
+    assert mean < 1.5 * tokens, (mean, tokens)
+    for a, b in zip(*grads):  # the two factors differ by the rounding of 1 / count at most
+        assert ((a - b).abs() <= 2.0 ** -22 * b.abs() + 2.0 ** -22 * b.abs().max()).all()
