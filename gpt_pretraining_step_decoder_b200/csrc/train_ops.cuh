@@ -297,12 +297,11 @@ static int ce_piece(int N, int V, int d, int dtype, int asked, int sms) {
   auto waves = [&](long long t) { return (double)((t + units - 1) / units); };
   int best = most;
   double best_cost = 1e300;
-  for (int w = most; w >= (most + 1) / 2; --w) {
-    double cost = 0.0;
-    for (int v = 0; v < tiles; v += w) {
-      const int n = std::min(w, tiles - v);
-      cost += waves((long long)n * cdiv(N, 256)) * d + waves((long long)n * cdiv(d, 256)) * N;
-    }
+  auto products = [&](int n) { return n ? waves((long long)n * cdiv(N, 256)) * d + waves((long long)n * cdiv(d, 256)) * N : 0.0; };
+  // every width of up to 512 tiles, at most 256 of more (the choice runs with every call)
+  const int step = std::max(1, most / 512);
+  for (int w = most; w >= (most + 1) / 2; w -= step) {
+    double cost = tiles / w * products(w) + products(tiles % w);
     cost += cdiv(tiles, w) * (waves((long long)cdiv(N, 256) * cdiv(d, 256)) * 0.04 * 256 * w);  // dx read and written
     if (cost < best_cost) { best_cost = cost; best = w; }
   }

@@ -103,3 +103,16 @@ def test_ce_of_no_rows_with_empty_outputs():
         assert st != g.GPT_ERR_ARG or "device" in g.gpt_last_error()
     assert ce_forward(loss=None, tok=None, lse=None) == g.GPT_ERR_ARG
     assert ce_backward(dx=None, dw=None) == g.GPT_ERR_ARG
+
+
+@pytest.mark.parametrize("N,V", [(1000, 10_000_000), (1, 1 << 30), (64, 1 << 28)])
+def test_choice_of_the_vocabulary_pieces_is_quick(N, V):
+    """Every gradient call chooses its pieces; a huge vocabulary of few rows must not
+    cost more host time than a launch does."""
+    import time
+    best = 1.0
+    for _ in range(50):
+        t0 = time.perf_counter()
+        g.linear_ce_workspace_bytes(N, V, 64, g.DTYPE_BF16, 1)
+        best = min(best, time.perf_counter() - t0)
+    assert best < 40e-6, best
