@@ -98,6 +98,15 @@ enum KMode {
 };
 __host__ __device__ constexpr bool is_lse(int km) { return km == K_LSE || km == K_LSE_WIDE; }
 __host__ __device__ constexpr bool is_dlogits(int km) { return km == K_DLOGITS || km == K_DLOGITS_WIDE; }
+// K goes through tensor memory in chunks whose sums are added in registers: the tensor
+// cores' fp32 accumulation truncates, always towards zero.  F8 = 2: where the sum
+// leaves in fp32 (relative L2 off fp64, 4096 x 2048 x 16384, operands of both signs /
+// positive: 2.4e-6 / 1.0e-5 in one chunk, 6.9e-7 / 5.8e-7 in chunks of 2048, 3.0e-7 / 8.6e-7
+// an fp32 product; 8192 x 2048 x 16384 takes 213 us instead of 203).  A bf16 result has
+// its own rounding of up to 2^-8, which that does not show in: one chunk.
+__host__ __device__ constexpr bool is_chunked(int km, int f8) {
+  return is_lse(km) || (f8 == 2 && (km == K_STORE_F32 || km == K_REDUCE_F32 || km == K_PARTIAL));
+}
 constexpr float WIDE_CAP = 64.f;
 
 // The ReLU^2-backward epilogue streams activations through a ring of its
@@ -150,7 +159,7 @@ struct Params {
   // row atoms per k-quad
   CUtensorMap tm_sfa, tm_sfb;
   int a_atoms, b_atoms;
-  int k_chunk; // K_LSE: k-blocks accumulated in tensor memory before the sum moves on to registers
+  int k_chunk; // is_chunked: k-blocks accumulated in tensor memory before the sum moves on to registers
   int a_skip;  // bytes of a stage's A tile that are not loaded (a product of fewer than 128 rows)
 };
 
@@ -497,6 +506,15 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[3
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
@@ -828,8 +846,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int split = RUNS ? 0 : (B3 ? t % per_product : t) % p.splits;
         const int kb0 = split * p.kb_per_split;
         const int kb1 = min(kb0 + p.kb_per_split, p.kb_total);
-        // one accumulator per chunk of K (K_LSE; else all of K is one chunk)
-        const int chunk = RUNS ? p.k_chunk : kb1 - kb0;
+        // one accumulator per chunk of K
+        const int chunk = is_chunked(KM, F8) ? p.k_chunk : kb1 - kb0;
         for (int kc = kb0; kc < kb1; kc += chunk) {
           const int kc1 = min(kc + chunk, kb1);
           if (!warp_wait(&tempty[acc], acc_phase ^ 1, abort_flag, p.err)) { ok = false; break; }
@@ -992,24 +1010,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           else mbar_arrive(&tempty[acc]);
         }
       }
-      if constexpr (is_lse(KM)) {
-        // The tensor cores' fp32 accumulation truncates, always towards zero, so the
-        // largest logits of a long K come out low (lse off by 1.2e-6 of its value at
-        // d = 1900): K goes through tensor memory in chunks whose sums are added
-        // here, rounded to nearest.  The accumulators take turns, so the
-        // next chunk is multiplied meanwhile.
-        for (int kc = p.k_chunk; kc < p.kb_total; kc += p.k_chunk) {
+      if constexpr (is_chunked(KM, F8)) {
+        // the chunks after the first, added rounded to nearest (in one chunk the
+        // largest logits of a long K come out low, lse off by 1.2e-6 of its value at
+        // d = 1900).  Two accumulators take turns, so the next chunk is multiplied
+        // meanwhile; one is handed back once it is in registers.
+        const int kbs = RUNS ? p.kb_total : min(p.kb_per_split, p.kb_total - split * p.kb_per_split);
+        for (int kc = p.k_chunk; kc < kbs; kc += p.k_chunk) {
           if (++acc == C::NACC) { acc = 0; acc_phase ^= 1; }
           if (!warp_wait(&tfull[acc], acc_phase, abort_flag, p.err)) { ok = false; break; }
           tc_fence_after();
           const uint32_t tr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * BN + ccol;
 #pragma unroll
-          for (int q2 = 0; q2 < HALF / 32; ++q2) {
-            uint32_t r[32];
-            tmem_ld32_nowait(tr + q2 * 32, r);
+          for (int q2 = 0; q2 < HALF / 16; ++q2) {  // 16 columns at a time: 32 would spill
+            uint32_t r[16];
+            tmem_ld16_nowait(tr + q2 * 16, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) accr[q2 * 32 + i] += __uint_as_float(r[i]) * ealpha;
+            for (int i = 0; i < 16; ++i) accr[q2 * 16 + i] += __uint_as_float(r[i]) * ealpha;
           }
           tc_fence_before();
           __syncwarp();
@@ -1019,6 +1037,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         if (!ok) break;
+      }
+      if constexpr (is_lse(KM)) {
         // the half tile's row maximum and sum of exp(z - max), all from
         // registers: nothing but these two numbers leaves the tile
         if (e.softcap > 0.f) {

@@ -204,7 +204,7 @@ static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda,
   TRY(make_tmap_gen(&p.tm_sfa, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sa, dsa, ls, bsa, CU_TENSOR_MAP_SWIZZLE_NONE));
   TRY(make_tmap_gen(&p.tm_sfb, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, sb, dsb, ls, bsb, CU_TENSOR_MAP_SWIZZLE_NONE));
   p.a_atoms = cdiv(M, 128); p.b_atoms = cdiv(N, 128);
-  p.a_skip = 0; p.k_chunk = 0;
+  p.a_skip = 0;
   p.M = M; p.N = N; p.K = K; p.batch = 1;
   p.a_kmajor = 1; p.b_kmajor = 1;
   p.m_tiles = cdiv(M, CG * tc::BM);
@@ -213,6 +213,7 @@ static int gemm_f8b_launch(int M, int N, int K, const uint8_t* A, long long lda,
   p.kb_total = cdiv(K, 128);
   p.kb_per_split = 4 * cdiv(cdiv(p.kb_total, 4), splits);
   p.splits = cdiv(p.kb_total, p.kb_per_split);
+  p.k_chunk = cdiv(p.kb_per_split, cdiv(p.kb_per_split, 16));  // at most 2048 of K
   p.epi = e; p.partial = partial; p.err = err;
   const bool f32 = e.mode != EPI_STORE;
   if (p.splits > 1) {

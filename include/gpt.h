@@ -471,7 +471,9 @@ int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes);
  * C[m, n] = (beta ? C[m, n] : 0) + sum_k A[m, k] B[n, k] with A [M, K] and
  * B [N, K] (M, N, K >= 1) codes and scales as fp8_block_quantize leaves them, on the tcgen05
  * tensor cores, which apply the scales (kind::mxf8f6f4.block_scale, fp32
- * accumulation; SM pairs when gptx_set_gemm_cta_pairs is on).  lda, ldb: row
+ * accumulation, which cuts sums off towards zero: fp32 outputs add K in chunks of
+ * 2048, rounded to nearest, bf16 outputs round the whole sum; SM pairs when
+ * gptx_set_gemm_cta_pairs is on).  lda, ldb: row
  * pitches of the codes in bytes; what lies between K and the pitch is not read.
  * out_dtype: GPT_DTYPE_F32 or GPT_DTYPE_BF16 (beta only with F32), row pitch ldc
  * elements.  Addresses and row pitches are multiples of 16 bytes.  A long K with few

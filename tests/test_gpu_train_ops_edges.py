@@ -167,3 +167,71 @@ def test_counting_the_targets_does_not_grow_with_the_product(g):
     assert mean < 1.5 * tokens, (mean, tokens)
     for a, b in zip(*grads):  # the two factors differ by the rounding of 1 / count at most
         assert ((a - b).abs() <= 2.0 ** -22 * b.abs() + 2.0 ** -22 * b.abs().max()).all()
+
+
+# The tensor cores add the 32 (bf16: 16) products of an instruction to an fp32
+# accumulator and cut the sum off, always towards zero, so a long sum of positive products
+# comes out low: 64 instructions, the chunks that are added rounded, each lose
+# less than a step (2^-23) of a partial sum that grows evenly, 65 / 2 steps of the
+# whole, and the chunks' own additions half a step each.  In one chunk the products
+# below were 6.1e-6 (K = 16384) and 1.7e-5 (K = 32768) low.
+CHUNKED = 65 / 2 * 2.0 ** -23 + 16 * 2.0 ** -24
+
+
+def quantized_uniform(g, rows, cols, gen):
+    """Positive e4m3 operand: codes, scales and its values in fp64."""
+    import torch
+    x = torch.rand(rows, cols, generator=gen, device="cuda") + 0.01
+    q = torch.empty(rows, cols, dtype=torch.uint8, device="cuda")
+    s = torch.empty(g.fp8_block_scale_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+    g.fp8_block_quantize(x, g.DTYPE_F32, rows, cols, cols, False, q, cols, s)
+    scale = torch.exp2(g.fp8_block_scales(s, rows, cols).double() - 127)
+    return q, s, q.view(torch.float8_e4m3fn).double() * scale.repeat_interleave(128, 1)
+
+
+@pytest.mark.parametrize("pairs", [True, False])
+@pytest.mark.parametrize("M,N,K,split", [(4096, 2048, 16384, False), (2304, 2304, 32768, False), (1000, 1000, 16384, True)])
+def test_long_products_in_fp32_are_not_cut_off(g, M, N, K, split, pairs):
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    qa, sa, va = quantized_uniform(g, M, K, gen)
+    qb, sb, vb = quantized_uniform(g, N, K, gen)
+    ref = va @ vb.T
+    g.gptx_set_gemm_cta_pairs(pairs)
+    try:
+        n = g.gptx_gemm_fp8_block_workspace_bytes(M, N, K)
+        assert (n > 0) == split
+        ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
+        c = torch.full((M, N), 9.0, device="cuda")
+        for beta in (0, 1):
+            g.gptx_gemm_fp8_block(M, N, K, qa, K, sa, qb, K, sb, g.DTYPE_F32, c, N, beta, ws, n)
+            torch.cuda.synchronize()
+            err = (c.double() / (1 + beta) - ref) / ref
+            assert err.mean().abs() <= CHUNKED and err.square().mean().sqrt() <= CHUNKED, (err.mean(), err.abs().max())
+    finally:
+        g.gptx_set_gemm_cta_pairs(True)
+    assert g.ngram_sync_status() == g.GPT_OK
+
+
+@pytest.mark.parametrize("softcap", [0.0, 50.0, 100.0])
+@pytest.mark.parametrize("N,V", [(40, 520), (3000, 20000)])
+def test_long_logits_are_not_cut_off(g, N, V, softcap):
+    """d = 8192, logits of about 50, all products positive."""
+    import torch
+    d = 8192
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.rand(N, d, generator=gen, device="cuda").bfloat16()
+    w = (torch.rand(V, d, generator=gen, device="cuda") * (200.0 / d)).bfloat16()
+    t = torch.randint(0, V, (N,), generator=gen, device="cuda", dtype=torch.int32)
+    loss, tok, lse = ce_forward(g, x, w, t, softcap)
+    u = x.double() @ w.double().T
+    z = softcap * torch.tanh(u / softcap) if softcap else u
+    slope = 1 - (z / softcap).square() if softcap else 1.0
+    ref = torch.logsumexp(z, 1)
+    # the cut-off logits, the soft-cap's 2^-22 of the cap, an fp32 step of the exponents and of the result
+    tol = ((z - ref[:, None]).exp() * slope * u).sum(1) * CHUNKED + softcap * 2.0 ** -22 + 2.0 ** -23 * (ref + 8)
+    err = lse.double() - ref
+    assert err.mean().abs() <= tol.mean() and err.square().mean().sqrt() <= tol.square().mean().sqrt()
+    zt = z.gather(1, t.long()[:, None]).squeeze(1)
+    assert (tok.double() - (ref - zt)).square().mean().sqrt() <= 2 * tol.square().mean().sqrt()
+    assert g.ngram_sync_status() == g.GPT_OK
