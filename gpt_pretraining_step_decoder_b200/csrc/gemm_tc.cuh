@@ -99,13 +99,15 @@ enum KMode {
 __host__ __device__ constexpr bool is_lse(int km) { return km == K_LSE || km == K_LSE_WIDE; }
 __host__ __device__ constexpr bool is_dlogits(int km) { return km == K_DLOGITS || km == K_DLOGITS_WIDE; }
 // K goes through tensor memory in chunks whose sums are added in registers: the tensor
-// cores' fp32 accumulation truncates, always towards zero.  F8 = 2: where the sum
+// cores' fp32 accumulation truncates, always towards zero.  The cross entropy's logits
+// in both passes (logits of 50 from 8192 positive products came out 1.7e-3 low, and with them
+// the gradient's p = exp(z - lse) by that part of itself).  F8 = 2: where the sum
 // leaves in fp32 (relative L2 off fp64, 4096 x 2048 x 16384, operands of both signs /
 // positive: 2.4e-6 / 1.0e-5 in one chunk, 6.9e-7 / 5.8e-7 in chunks of 2048, 3.0e-7 / 8.6e-7
 // an fp32 product; 8192 x 2048 x 16384 takes 213 us instead of 203).  A bf16 result has
 // its own rounding of up to 2^-8, which that does not show in: one chunk.
 __host__ __device__ constexpr bool is_chunked(int km, int f8) {
-  return is_lse(km) || (f8 == 2 && (km == K_STORE_F32 || km == K_REDUCE_F32 || km == K_PARTIAL));
+  return is_lse(km) || is_dlogits(km) || (f8 == 2 && (km == K_STORE_F32 || km == K_REDUCE_F32 || km == K_PARTIAL));
 }
 constexpr float WIDE_CAP = 64.f;
 

@@ -509,7 +509,7 @@ int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int 
  * ignored and set GPT_ERR_INPUT on the standalone error word, a mean that is not
  * finite GPT_ERR_NONFINITE (ngram_sync_status).  loss, tok_loss [N], lse [N]: device
  * float, each nullable; keep lse for the backward pass.  The logits are formed
- * in tiles on the tensor cores with fp32 accumulation and reduced there (fp32 mode:
+ * in tiles on the tensor cores with fp32 accumulation (d in chunks of 1024) and reduced there (fp32 mode:
  * FFMA, a piece of fp32 logits at a time in the workspace); sums are formed
  * in a fixed order.  N = 0 gives a loss of 0; the addresses of its [0]-sized tensors may
  * be null, here and in the backward pass (which leaves dW = 0, or as it was with dw_beta).  workspace: 256-byte aligned.

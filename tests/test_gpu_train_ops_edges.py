@@ -235,3 +235,45 @@ def test_long_logits_are_not_cut_off(g, N, V, softcap):
     zt = z.gather(1, t.long()[:, None]).squeeze(1)
     assert (tok.double() - (ref - zt)).square().mean().sqrt() <= 2 * tol.square().mean().sqrt()
     assert g.ngram_sync_status() == g.GPT_OK
+
+
+@pytest.mark.parametrize("softcap", [0.0, 50.0, 100.0])
+@pytest.mark.parametrize("N,V", [(40, 520), (3000, 20000)])
+def test_gradient_of_long_logits_sums_to_zero(g, N, V, softcap):
+    """d = 8192, all products positive: sum_v dz / slope is 0 for a softmax; with a column
+    of ones in W and no soft-cap it is dx of that column.  With a soft-cap the column of
+    dx is compared with fp64."""
+    import torch
+    d = 8192
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.rand(N, d, generator=gen, device="cuda").bfloat16()
+    w = (torch.rand(V, d, generator=gen, device="cuda") * (200.0 / d)).bfloat16()
+    w[:, 0] = 1.0
+    t = torch.randint(0, V, (N,), generator=gen, device="cuda", dtype=torch.int32)
+    u = x.double() @ w.double().T
+    z = softcap * torch.tanh(u / softcap) if softcap else u
+    slope = 1 - (z / softcap).square() if softcap else torch.ones_like(u)
+    lse = torch.logsumexp(z, 1)
+    p = (z - lse[:, None]).exp()
+    dz = p * slope
+    at = t.long()[:, None]
+    dz.scatter_add_(1, at, -slope.gather(1, at))
+    ref = dz.sum(1)
+    # every p is off by that of its logit; dz is rounded to bf16 (at random, but for the
+    # target's term), and its sum of V / 16 additions cut off below a step of a sum below one
+    ez = slope * u * CHUNKED + softcap * 2.0 ** -22 + 2.0 ** -23 * (lse[:, None].abs() + 8)
+    if softcap:  # and the slope, 2^-22 of tanh
+        ez = ez + 2.0 ** -21 / slope
+    tol = (p * slope * ez).sum(1) + slope.gather(1, at).squeeze(1) * 2.0 ** -21
+    tol += 4 * 2.0 ** -9 * (dz.square().sum(1) - dz.gather(1, at).squeeze(1).square()).clamp(min=0).sqrt()
+    tgt = dz.gather(1, at).squeeze(1)
+    tol += (tgt.bfloat16().double() - tgt).abs() + (V / 16 + 16) * 2.0 ** -23 * (p * slope).sum(1) + 2.0 ** -8 * ref.abs()
+    n = g.linear_ce_workspace_bytes(N, V, d, g.DTYPE_BF16, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    dx, dtok, lse32 = torch.empty_like(x), torch.ones(N, device="cuda"), lse.float()
+    g.linear_ce_backward(x, d, w, d, g.DTYPE_BF16, N, V, d, t, softcap, lse32, None, dtok, dx, d, None, d, g.DTYPE_BF16, 0,
+                         ws, n)
+    torch.cuda.synchronize()
+    err = dx[:, 0].double() - ref
+    assert err.mean().abs() <= tol.mean() and err.square().mean().sqrt() <= tol.square().mean().sqrt(), (err.mean(), tol.mean())
+    assert g.ngram_sync_status() == g.GPT_OK
