@@ -93,6 +93,8 @@ _SIGS = {
     "fp8_block_quantize": [_P, _I, _LL, _LL, _LL, _I, _P, _LL, _P, _P, _LL, _P, _P],
     "gptx_gemm_fp8_block_workspace_bytes": [_I, _I, _I, ctypes.POINTER(_SZ)],
     "gptx_gemm_fp8_block": [_I, _I, _I, _P, _LL, _P, _P, _LL, _P, _I, _P, _LL, _I, _P, _SZ, _P],
+    "gptx_gemm_fp8_block_plan": [_I, _I, _I, ctypes.POINTER(_I)],
+    "linear_ce_plan": [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_I)],
     "linear_ce_workspace_bytes": [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)],
     "linear_ce_forward": [_P, _LL, _P, _LL, _I, _I, _I, _I, _P, _F, _P, _P, _P, _I, _P, _SZ, _P],
     "linear_ce_backward": [_P, _LL, _P, _LL, _I, _I, _I, _I, _P, _F, _P, _P, _P, _P, _LL, _P, _LL, _I, _I, _I, _P,
@@ -368,6 +370,13 @@ def gptx_gemm_fp8_block_workspace_bytes(M, N, K):
     return n.value
 
 
+def gptx_gemm_fp8_block_plan(M, N, K):
+    """(columns of a tile, SMs per tile, shares of K) of such a product."""
+    p = (ctypes.c_int * 3)()
+    _check(_lib.gptx_gemm_fp8_block_plan(M, N, K, p), "gptx_gemm_fp8_block_plan")
+    return tuple(p)
+
+
 def gptx_gemm_fp8_block(M, N, K, A, lda, scales_a, B, ldb, scales_b, out_dtype, C, ldc, beta=0, workspace=None,
                         ws_bytes=0, stream=None):
     """C [M, N] (+)= A B^T of two matrices quantized by fp8_block_quantize."""
@@ -381,6 +390,15 @@ def linear_ce_workspace_bytes(N, V, d, dtype, backward, vocab_piece=0):
     _check(_lib.linear_ce_workspace_bytes(N, V, d, dtype, int(backward), vocab_piece, ctypes.byref(b)),
            "linear_ce_workspace_bytes")
     return b.value
+
+
+def linear_ce_plan(N, V, d, dtype, backward, vocab_piece=0):
+    """The forms of linear_ce_forward / linear_ce_backward: dict of the vocabulary's
+    piece, the logits' product (columns of a tile, SMs per tile, tiles per run) and
+    dx's and dW's (columns of a tile, SMs per tile, shares of K)."""
+    p = (ctypes.c_int * 10)()
+    _check(_lib.linear_ce_plan(N, V, d, dtype, int(backward), vocab_piece, p), "linear_ce_plan")
+    return {"piece": p[0], "logits": tuple(p[1:4]), "dx": tuple(p[4:7]), "dw": tuple(p[7:10])}
 
 
 def linear_ce_forward(x, ldx, w, ldw, dtype, N, V, d, targets, softcap, loss, tok_loss, lse, workspace, ws_bytes,

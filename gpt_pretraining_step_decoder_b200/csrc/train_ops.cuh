@@ -244,6 +244,14 @@ extern "C" int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* 
   return GPT_OK;
 }
 
+extern "C" int gptx_gemm_fp8_block_plan(int M, int N, int K, int* plan) {
+  if (!plan || M < 1 || N < 1 || K < 1 || M > MAX_ROWS || N > MAX_ROWS || K > MAX_ROWS)
+    return fail(GPT_ERR_ARG, "gptx_gemm_fp8_block_plan: bad argument");
+  const F8bPlan pl = f8b_plan(M, N, K, device_sms());
+  plan[0] = pl.bn; plan[1] = pl.cg; plan[2] = pl.splits;
+  return GPT_OK;
+}
+
 extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long long lda, const uint8_t* scales_a,
                                    const uint8_t* B, long long ldb, const uint8_t* scales_b, int out_dtype, void* C,
                                    long long ldc, int beta, void* workspace, size_t ws_bytes, void* stream) {
@@ -397,6 +405,27 @@ extern "C" int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int bac
   if (!bytes || N < 0 || V < 1 || d < 1 || N > MAX_ROWS || V > MAX_ROWS || d > MAX_ROWS || vocab_piece < 0 || (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16))
     return fail(GPT_ERR_ARG, "linear_ce_workspace_bytes: bad argument");
   *bytes = ce_ws_plan(N, V, d, dtype, backward != 0, vocab_piece, device_sms()).total;
+  return GPT_OK;
+}
+
+extern "C" int linear_ce_plan(int N, int V, int d, int dtype, int backward, int vocab_piece, int* plan) {
+  if (!plan || N < 1 || V < 1 || d < 1 || N > MAX_ROWS || V > MAX_ROWS || d > MAX_ROWS || vocab_piece < 0 ||
+      (dtype != GPT_DTYPE_F32 && dtype != GPT_DTYPE_BF16))
+    return fail(GPT_ERR_ARG, "linear_ce_plan: bad argument");
+  const int sms = device_sms();
+  const CeWs w = ce_ws_plan(N, V, d, dtype, backward != 0, vocab_piece, sms);
+  const TilePlan none{0, 0, 0, 0};
+  TilePlan logits = w.lse, dx = none, dw = none;
+  if (dtype == GPT_DTYPE_F32) {
+    logits = none;
+  } else if (backward) {
+    logits = tile_plan(N, w.piece, d, 0, sms);
+    dx = tile_plan(N, d, w.piece, w.splitk_elems, sms);
+    dw = tile_plan(w.piece, d, N, w.splitk_elems, sms);
+  }
+  const int out[] = {!backward && dtype == GPT_DTYPE_BF16 ? V : w.piece, logits.bn, logits.cg, logits.n_run,
+                     dx.bn, dx.cg, dx.splits, dw.bn, dw.cg, dw.splits};
+  for (int i = 0; i < 10; ++i) plan[i] = out[i];
   return GPT_OK;
 }
 

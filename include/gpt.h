@@ -467,6 +467,10 @@ int fp8_block_quantize(const void* x, int dtype, long long rows, long long cols,
  * device that is current (the call plans for its tensors' device). */
 int gptx_gemm_fp8_block_workspace_bytes(int M, int N, int K, size_t* bytes);
 
+/* The form in which gptx_gemm_fp8_block() runs such a product, under the same
+ * conditions: plan[3] = columns of a tile, SMs that share one, shares of K.  Host only. */
+int gptx_gemm_fp8_block_plan(int M, int N, int K, int* plan);
+
 /*
  * C[m, n] = (beta ? C[m, n] : 0) + sum_k A[m, k] B[n, k] with A [M, K] and
  * B [N, K] (M, N, K >= 1) codes and scales as fp8_block_quantize leaves them, on the tcgen05
@@ -496,6 +500,15 @@ int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long long lda, co
  * on the device that is current (the call plans for its tensors' device).
  */
 int linear_ce_workspace_bytes(int N, int V, int d, int dtype, int backward, int vocab_piece, size_t* bytes);
+
+/*
+ * The forms in which the two calls run, under the same conditions: plan[10] = columns of
+ * the vocabulary taken at a time; for bf16 (0 for fp32) of the logits' product the
+ * columns of a tile, SMs that share one and (forward) tiles in a run whose statistics
+ * stay in registers; for the backward pass of the products of dx and of dW (of the first
+ * piece) columns of a tile, SMs that share one, shares of K.  Host only.
+ */
+int linear_ce_plan(int N, int V, int d, int dtype, int backward, int vocab_piece, int* plan);
 
 /*
  * Loss of the LM head on the caller's hidden states ("$1000 tier nanochat run",
