@@ -170,14 +170,14 @@ static F8bPlan f8b_plan(int M, int N, int K, int sms) {
   double best_t = 1e300;
   for (int cg = 1; cg <= (M > 128 && gemm_pairs_enabled() ? 2 : 1); ++cg)
     for (int bn : {128, 256}) {
-      if (bn == 256 && N <= 128) continue;
+      if (bn == 256 ? N <= 128 : cg == 2) continue;  // pairs of 128 columns start later and load no less
       const long long tiles = (long long)cdiv(M, 128 * cg) * cdiv(N, bn), units = sms / cg;
       for (int s = 1; s <= (N % 4 == 0 && tiles < units ? std::min(32, quads) : 1); ++s) {
         const int share = cdiv(quads, s);
         if (cdiv(quads, share) != s) continue;  // the same shares as a smaller split
         const double busy = std::min(1.0, (double)(tiles * s) / units);  // share of the SMs that load
-        const double c = cg == 2 ? (bn == 256 ? 0.345 : 0.30) : (bn == 256 ? 0.31 + 0.16 * busy : 0.30);
-        const double e = cg == 2 ? (bn == 256 ? 1.45 : 0.65) : (bn == 256 ? 1.17 : 0.65);
+        const double c = cg == 2 ? 0.345 : bn == 256 ? 0.31 + 0.16 * busy : 0.30;
+        const double e = cg == 2 ? 1.45 : bn == 256 ? 1.17 : 0.65;
         const double waves = (double)((tiles * s + units - 1) / units);
         const double t = (cg == 2 ? 4.2 : 3.2) + waves * (std::min(kb, 4 * share) * c + e) +
                          (s > 1 ? 1.5 + (double)s * M * N * 8e-7 : 0.0);
@@ -285,7 +285,7 @@ extern "C" int gptx_gemm_fp8_block(int M, int N, int K, const uint8_t* A, long l
 #define F8B(BN, CG) \
   gemm_f8b_launch<BN, CG>(M, N, K, A, lda, scales_a, B, ldb, scales_b, e, pl.splits, part, err, st)
   if (pl.bn == 256) return pl.cg == 2 ? F8B(256, 2) : F8B(256, 1);
-  return pl.cg == 2 ? F8B(128, 2) : F8B(128, 1);
+  return F8B(128, 1);
 #undef F8B
 }
 
