@@ -67,6 +67,7 @@
 // own TMA copies in flight and frees its TMEM before returning.
 #pragma once
 #include <cuda.h>
+#include <type_traits>
 #include "gemm_common.cuh"
 
 namespace tc {
@@ -1343,6 +1344,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             o.z = *reinterpret_cast<uint32_t*>(&b2);
             o.w = *reinterpret_cast<uint32_t*>(&b3);
             *reinterpret_cast<uint4*>(stg + swz128(lane, j)) = o;
+          }
+        }
+        if constexpr (!B3 && (KM == K_STORE || KM == K_STORE_F32 || KM == K_REDUCE_F32)) {
+          // a TMA store that ends inside 16 bytes writes them all, columns behind the
+          // last among them: such a block's rows go out element by element
+          using out_t = typename std::conditional<f32out, float, bf16>::type;
+          constexpr int PER = 16 / (int)sizeof(out_t);
+          if (p.N % PER != 0 && nc + CW > p.N) {  // warp-uniform
+            if (m < p.M) {
+              out_t* row = reinterpret_cast<out_t*>(e.C) + m * e.ldc + nc;
+#pragma unroll 1
+              for (int i = 0; i < p.N - nc; ++i) {
+                const out_t x = reinterpret_cast<const out_t*>(stg + swz128(lane, i / PER))[i % PER];
+                if constexpr (KM == K_REDUCE_F32) row[i] += x;
+                else row[i] = x;
+              }
+            }
+            return true;
           }
         }
         fence_async_smem();

@@ -420,7 +420,7 @@ int fp8_quantize(const void* x, int dtype, long long n, uint8_t* q, float* scale
  * multiples of 16) on the tcgen05 tensor cores (kind::f8f6f4, fp32
  * accumulation; SM pairs when gptx_set_gemm_cta_pairs is on).  out_dtype:
  * GPT_DTYPE_F32 or GPT_DTYPE_BF16 for C (device, row pitch ldc elements, 16-byte
- * aligned).  Asynchronous on `stream`.
+ * aligned; columns between N and ldc are left as they are).  Asynchronous on `stream`.
  */
 int gptx_gemm_fp8(int M, int N, int K, const uint8_t* A, long long lda, const uint8_t* B, long long ldb,
                   const float* scale_a, const float* scale_b, int out_dtype, void* C, long long ldc, void* stream);
@@ -480,7 +480,8 @@ int gptx_gemm_fp8_block_plan(int M, int N, int K, int* plan);
  * gptx_set_gemm_cta_pairs is on).  lda, ldb: row
  * pitches of the codes in bytes; what lies between K and the pitch is not read.
  * out_dtype: GPT_DTYPE_F32 or GPT_DTYPE_BF16 (beta only with F32), row pitch ldc
- * elements.  Addresses and row pitches are multiples of 16 bytes.  A long K with few
+ * elements; columns between N and ldc are left as they are.  Addresses and row pitches
+ * are multiples of 16 bytes.  A long K with few
  * output tiles is split, its fp32 partials (in `workspace`, 256-byte aligned) summed in
  * order: the result is bit-reproducible.  Asynchronous on `stream`; a bounded
  * wait that gives up is reported by ngram_sync_status().
@@ -627,7 +628,9 @@ int muon_update(float* W, float* M, const float* G, int rows, int cols, int out_
  * (a_kmajor = 0: at A[k*lda + m]); B likewise with N.  splits > 1 (modes 1 and
  * 2 only) splits K and needs workspace of splits*M*N*4 bytes, the partials
  * being summed in split order.  Operands, C and aux must be 16-byte aligned
- * with row pitches that are multiples of 16 bytes.  Asynchronous on `stream`.
+ * with row pitches that are multiples of 16 bytes.  Columns of C between N and ldc are
+ * left as they are in modes 0 to 2; modes 3 to 5 write whole 16-byte pieces of a row.
+ * Asynchronous on `stream`.
  */
 int gptx_gemm_bf16(int M, int N, int K, const void* A, long long lda, int a_kmajor, const void* B,
                    long long ldb, int b_kmajor, int mode, void* C, long long ldc, const void* aux,

@@ -277,3 +277,50 @@ def test_gradient_of_long_logits_sums_to_zero(g, N, V, softcap):
     err = dx[:, 0].double() - ref
     assert err.mean().abs() <= tol.mean() and err.square().mean().sqrt() <= tol.square().mean().sqrt(), (err.mean(), tol.mean())
     assert g.ngram_sync_status() == g.GPT_OK
+
+
+@pytest.fixture(params=[True, False], ids=["sm_pairs", "one_sm"])
+def pairs(request, g):
+    g.gptx_set_gemm_cta_pairs(request.param)
+    yield request.param
+    g.gptx_set_gemm_cta_pairs(True)
+
+
+def e4m3(rows, K, seed):
+    """Codes [rows, pitch] of values in (-2, 2) that fill fp32 sums exactly, and the values."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    v = torch.randint(-4, 5, (rows, K), generator=gen, device="cuda").double() / 4
+    q = torch.zeros(rows, -(-K // 16) * 16, dtype=torch.uint8, device="cuda")
+    q[:, :K] = v.float().to(torch.float8_e4m3fn).view(torch.uint8)
+    return q, v
+
+
+@pytest.mark.parametrize("M,N", [(33, 5), (300, 333), (70, 127), (1000, 1001), (9001, 2315)])
+@pytest.mark.parametrize("op", ["block", "block_beta", "tensor", "bf16", "bf16_beta"])
+def test_products_leave_the_columns_behind_an_odd_width(g, pairs, op, M, N):
+    """A result as some columns of a wider matrix, its last ones inside 16 bytes: the
+    neighbours stay.  Small whole numbers of quarters: every sum is exact."""
+    import torch
+    K = 264
+    (qa, va), (qb, vb) = e4m3(M, K, M), e4m3(N, K, N)
+    ref = va @ vb.T
+    for dt in (torch.float32, torch.bfloat16):
+        beta = op.endswith("beta")
+        if beta and dt == torch.bfloat16:
+            continue
+        ld, code = N + 16 - N % 8 + 8, g.DTYPE_F32 if dt == torch.float32 else g.DTYPE_BF16
+        c = torch.full((M + 1, ld), 7.0, dtype=dt, device="cuda")
+        one = torch.ones(1, device="cuda")
+        if op.startswith("block"):
+            sa, sb = (torch.full((g.fp8_block_scale_bytes(r, K),), 127, dtype=torch.uint8, device="cuda") for r in (M, N))
+            g.gptx_gemm_fp8_block(M, N, K, qa, qa.shape[1], sa, qb, qb.shape[1], sb, code, c, ld, beta)
+        elif op == "tensor":
+            g.gptx_gemm_fp8(M, N, K, qa, qa.shape[1], qb, qb.shape[1], one, one, code, c, ld)
+        else:
+            mode = 0 if dt == torch.bfloat16 else 2 if beta else 1
+            g.gptx_gemm_bf16(M, N, K, va.bfloat16(), K, 1, vb.bfloat16(), K, 1, c, ld, beta=int(beta), mode=mode)
+        torch.cuda.synchronize()
+        assert (c[M:] == 7).all() and (c[:, N:] == 7).all()
+        assert torch.equal(c[:M, :N], (ref + 7 * beta).to(dt))
+    assert g.ngram_sync_status() == g.GPT_OK
