@@ -21,7 +21,9 @@
 #pragma once
 #include "common.cuh"
 
-constexpr int CLIP_BLOCKS = 1184;        // 8 resident blocks on each of 148 SMs
+// blocks of a launch at most, and partials it leaves: 8 for each of 148 SMs, where 6 (sums,
+// 38 registers) and 3 (scaling, 79) are resident at a time; the others follow behind them
+constexpr int CLIP_BLOCKS = 1184;
 constexpr int CLIP_THREADS = 256;
 constexpr int CLIP_PIECE = 32768;        // bytes: eight 16-byte loads a thread, all in flight
 constexpr int CLIP_MAX_TENSORS = 1024;   // a launch (28 KB of kernel parameters)

@@ -91,7 +91,7 @@ enum KMode {
   K_LSE,          // no output: row statistics of z = softcap(acc) per half tile, target logit
   K_DLOGITS,      // bf16 gradient of the cross entropy with respect to the logits
   K_AXPBY,        // bf16 acc + aux_scale * aux (aux streamed like the ReLU^2 backward's)
-  // The same two for caps above WIDE_CAP (tanh_block).  Kernels of their own: with
+  // K_LSE and K_DLOGITS for caps above WIDE_CAP (tanh_block).  Kernels of their own: with
   // the series beside the quick form, the loss of 32768 x 50304 x 768 without a cap
   // went from 1770 to 1840 us (registers).
   K_LSE_WIDE,
@@ -561,9 +561,9 @@ __device__ __forceinline__ void softcap_block(float (&v)[NVAL], float cap) {
 // is off by cap 2^-22: 1.5e-5 at WIDE_CAP = 64, but 0.2 at 10^6.  Above it (WIDE) the
 // quotients below 1/2 take tanh's Taylor series through the 13th power (next
 // term 9e-8 of the value there), whose error is relative.  Through __expf and
-// __fdividef, as softcap_block, the loss of 32768 x 50304 x 768 with a cap took 2164 us
-// instead of 2131, the gradient of 16384 x 65536 x 2048 11015 instead of 10922; WIDE's
-// loss takes 3430 us (12 more instructions an element).
+// __fdividef, as softcap_block, the loss of 32768 x 50304 x 768 with a cap took 1.5% longer,
+// the gradient of 16384 x 65536 x 2048 0.9%.  That loss takes 2070 us, WIDE's 3450 (12 more
+// instructions an element), 1780 without a cap.
 template <int NVAL, bool WIDE>
 __device__ __forceinline__ void tanh_block(float (&v)[NVAL], float cap) {
   const float c = 2.f * 1.4426950408889634f / cap;

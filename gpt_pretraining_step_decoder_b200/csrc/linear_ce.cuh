@@ -15,8 +15,8 @@
 // common, dz = -(1 - p) with p near 0 is then exact instead of off by the same
 // half step in every row.  Three products of 2 N V d
 // operations bound it.  B200, in a stream of calls: 32768 x 50304 x 768 forward
-// 1877 us (1349 TFLOP/s), 16384 x 65536 x 2048 backward with soft-cap 10.7 ms (1239
-// TFLOP/s, under the power cap; 9.4 ms in a short run), 33 x 50304 x 768 forward 23.0 us
+// 1868 us (1355 TFLOP/s), 16384 x 65536 x 2048 backward with soft-cap 10.7 ms (1233
+// TFLOP/s, under the power cap; 9.2 ms in a short run), 33 x 50304 x 768 forward 23.6 us
 // (17.6 of them the one read of W, 4.4 TB/s).  fp32: the same pieces through plain FFMA products, with
 // fp32 logits of one piece at a time in the workspace.
 #pragma once

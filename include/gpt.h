@@ -540,7 +540,7 @@ int linear_ce_forward(const void* x, long long ldx, const void* w, long long ldw
  * with g[i] = *dloss / (number of targets that are not ignored) (dloss null: 1),
  * or g[i] = dtok[i] when dtok (device float [N], the gradient of tok_loss) is given;
  * not both.  Ignored rows get dx = 0; their x must be finite (it enters dW times
- * zero).  dx: [N, d] of `dtype`, row pitch lddx; dw: [V, d] of dw_dtype (bf16
+ * zero), and in bf16 *dloss (it multiplies the finished products).  dx: [N, d] of `dtype`, row pitch lddx; dw: [V, d] of dw_dtype (bf16
  * inputs: BF16 or F32; fp32 inputs: F32), row pitch lddw, overwritten or, with
  * dw_beta != 0 (F32 only), added to; either gradient may be null.  dz of a piece is
  * rounded to bf16 for the tensor cores (as the training step does) and dx
