@@ -324,3 +324,156 @@ def test_products_leave_the_columns_behind_an_odd_width(g, pairs, op, M, N):
         assert (c[M:] == 7).all() and (c[:, N:] == 7).all()
         assert torch.equal(c[:M, :N], (ref + 7 * beta).to(dt))
     assert g.ngram_sync_status() == g.GPT_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (2, 3, 5), (129, 1, 127), (5, 129, 513), (1, 1, 4097), (257, 130, 8190)])
+def test_products_of_tiny_and_odd_sizes(g, pairs, M, N, K):
+    import torch
+    (qa, va), (qb, vb) = e4m3(M, K, M + K), e4m3(N, K, N + K)
+    sa, sb = (torch.full((g.fp8_block_scale_bytes(r, K),), 127, dtype=torch.uint8, device="cuda") for r in (M, N))
+    n = g.gptx_gemm_fp8_block_workspace_bytes(M, N, K)
+    ws = torch.empty(max(n, 256), dtype=torch.uint8, device="cuda")
+    for dt, code in ((torch.float32, g.DTYPE_F32), (torch.bfloat16, g.DTYPE_BF16)):
+        ld = -(-N // 8) * 8
+        c = torch.full((M, ld), 7.0, dtype=dt, device="cuda")
+        g.gptx_gemm_fp8_block(M, N, K, qa, qa.shape[1], sa, qb, qb.shape[1], sb, code, c, ld, 0, ws, n)
+        torch.cuda.synchronize()
+        assert torch.equal(c[:, :N], (va @ vb.T).to(dt)) and (c[:, N:] == 7).all()
+    assert g.ngram_sync_status() == g.GPT_OK
+
+
+def test_clip_partly_in_place(g):
+    """Outputs that are their own tensor beside others that are not."""
+    import torch
+    grads = [torch.randn(n, device="cuda") for n in (5000, 333, 70001)]
+    keep = [t.clone() for t in grads]
+    outs = [grads[0], torch.empty_like(grads[1]), grads[2]]
+    ws = torch.empty(g.grad_clip_workspace_bytes(3), dtype=torch.uint8, device="cuda")
+    norm = torch.zeros(1, device="cuda")
+    want = sum(t.double().square().sum() for t in keep).sqrt().item()
+    g.grad_clip(grads, outs, 0.25, norm, ws, ws.numel())
+    coef = 0.25 / (want + 1e-6)
+    for t, o in zip(keep, outs):
+        assert ((o.double() - t.double() * coef).abs() <= 2.0 ** -22 * t.double().abs() * coef).all()
+    assert torch.equal(grads[1], keep[1]) and abs(norm.item() - want) <= 2.0 ** -23 * want
+
+
+def test_two_threads(g):
+    """Every operator from two host threads, on streams, tensors and workspaces of their
+    own: the bits are those of a single thread."""
+    import torch
+    N, V, d = 500, 3000, 264
+
+    class Run:
+        def __init__(self, seed):
+            self.st = torch.cuda.Stream()
+            self.x, self.w, self.t = ce_inputs(N, V, d, seed)
+            self.ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+            new = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+            self.q, self.s = new(N, 272, dt=torch.uint8), new(g.fp8_block_scale_bytes(N, d), dt=torch.uint8)
+            self.qw, self.sw = new(V, 272, dt=torch.uint8), new(g.fp8_block_scale_bytes(V, d), dt=torch.uint8)
+            self.c, self.loss, self.lse = new(N, V), new(1), new(N)
+            self.dx, self.dw, self.norm = torch.zeros_like(self.x), torch.zeros_like(self.w), new(1)
+            self.outs = [torch.zeros_like(self.dx), torch.zeros_like(self.dw)]
+
+        def __call__(self):
+            st, ws, n, bf = self.st, self.ws, self.ws.numel(), g.DTYPE_BF16
+            g.fp8_block_quantize(self.x, bf, N, d, d, False, self.q, 272, self.s, stream=st)
+            g.fp8_block_quantize(self.w, bf, V, d, d, True, self.qw, 272, self.sw, stream=st)
+            g.gptx_gemm_fp8_block(N, V, d, self.q, 272, self.s, self.qw, 272, self.sw, g.DTYPE_F32, self.c, V, 0, ws, n, st)
+            g.linear_ce_forward(self.x, d, self.w, d, bf, N, V, d, self.t, 15.0, self.loss, None, self.lse, ws, n, st)
+            g.linear_ce_backward(self.x, d, self.w, d, bf, N, V, d, self.t, 15.0, self.lse, None, None, self.dx, d, self.dw,
+                                 d, bf, 0, ws, n, st)
+            g.grad_clip([self.dx, self.dw], self.outs, 1e-3, self.norm, ws, n, st)
+            st.synchronize()
+            return [t.clone() for t in (self.q, self.s, self.c, self.loss, self.lse, self.dx, self.dw, self.norm, *self.outs)]
+
+    runs = [Run(1), Run(2)]
+    torch.cuda.synchronize()
+    want = [r() for r in runs]
+    bad = []
+
+    def work(r, ref):
+        try:
+            for _ in range(60):
+                if not all(torch.equal(a, b) for a, b in zip(r(), ref)):
+                    bad.append("bits")
+        except Exception as e:  # noqa: BLE001 -- reported below
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(runs, want)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not bad and g.ngram_sync_status() == g.GPT_OK
+
+
+def test_offsets_beyond_32_bits(g):
+    """Row pitches that put the last rows of an operand or a result past 2^32 elements, a
+    gradient of more than 2^31, statistics of more than 2^31 pairs."""
+    import torch
+    big, ld = torch.empty(9 << 30, dtype=torch.uint8, device="cuda"), 1 << 20
+    # the quantizer: by TMA, and with rows off 16 bytes by plain loads
+    for pitch_, dt, code in ((ld, torch.bfloat16, 1), (ld + 1, torch.bfloat16, 1)):
+        rows, cols = 4200, 200
+        x = big.view(dt)[:rows * pitch_].view(rows, pitch_)[:, :cols]
+        x.copy_(torch.randn(rows, cols, device="cuda"))
+        y = x.contiguous()
+        out = []
+        for src, p in ((x, pitch_), (y, cols)):
+            q, s = torch.zeros(rows, 208, dtype=torch.uint8, device="cuda"), torch.zeros(g.fp8_block_scale_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+            g.fp8_block_quantize(src, code, rows, cols, p, False, q, 208, s)
+            out += [q, s]
+        assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
+    # the product: operands and results, plain and element by element at the row's end
+    M, K = 8300, 264
+    (qa, va), (qb, vb) = e4m3(M, K, 1), e4m3(141, K, 2)
+    sa, sb = (torch.full((g.fp8_block_scale_bytes(r, K),), 127, dtype=torch.uint8, device="cuda") for r in (M, 141))
+    a = big[:M * ld].view(M, ld)
+    a[:, :K] = qa[:, :K]
+    for N in (136, 141):
+        c = torch.zeros(M, 144, device="cuda")
+        g.gptx_gemm_fp8_block(M, N, K, a, ld, sa, qb, qb.shape[1], sb, g.DTYPE_F32, c, 144)
+        assert torch.equal(c[:, :N].double(), va @ vb[:N].T)
+        wide = big.view(torch.bfloat16)[:4200 * ld].view(4200, ld)
+        wide[:, N:160] = 7
+        g.gptx_gemm_fp8_block(4200, N, K, qa, qa.shape[1], torch.full((g.fp8_block_scale_bytes(4200, K),), 127, dtype=torch.uint8, device="cuda"),
+                              qb, qb.shape[1], sb, g.DTYPE_BF16, wide, ld)
+        assert torch.equal(wide[:, :N], (va[:4200] @ vb[:N].T).bfloat16()) and (wide[:, N:160] == 7).all()
+        a[:, :K] = qa[:, :K]                       # the result lay over it
+    # the loss and its gradient
+    N, V, d = 4200, 3000, 64
+    x, w, t = ce_inputs(N, V, d)
+    xs = big.view(torch.bfloat16)[:N * ld].view(N, ld)[:, :d]
+    xs.copy_(x)
+    ref = ce_forward(g, x, w, t)
+    n = max(g.linear_ce_workspace_bytes(N, V, d, g.DTYPE_BF16, b) for b in (0, 1))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    loss, tok, lse = (torch.zeros_like(r) for r in ref)
+    g.linear_ce_forward(xs, ld, w, d, g.DTYPE_BF16, N, V, d, t, 0.0, loss, tok, lse, ws, n)
+    assert all(torch.equal(p, q) for p, q in zip((loss, tok, lse), ref))
+    dx, dw, dw2 = torch.zeros_like(x), torch.zeros_like(w), torch.zeros_like(w)
+    g.linear_ce_backward(x, d, w, d, g.DTYPE_BF16, N, V, d, t, 0.0, lse, None, None, dx, d, dw, d, g.DTYPE_BF16, 0, ws, n)
+    g.linear_ce_backward(x, d, w, d, g.DTYPE_BF16, N, V, d, t, 0.0, lse, None, None, xs, ld, dw2, d, g.DTYPE_BF16, 0, ws, n)
+    assert torch.equal(xs, dx) and torch.equal(dw, dw2)
+    # the clip
+    v = big.view(torch.bfloat16)[:(1 << 31) + 77777]
+    v.fill_(0.5)
+    v[-1] = 3.0
+    norm = torch.zeros(1, device="cuda")
+    g.grad_clip([v], None, 1.0, norm, ws, n)
+    want = (0.25 * (v.numel() - 1) + 9) ** 0.5
+    assert abs(norm.item() - want) <= 2.0 ** -23 * want
+    assert abs(v[-1].item() - 3 / want) <= 2.0 ** -8 * 3 / want and (v[:-1] == v[0]).all()
+    del big, a, wide, xs, v
+    # the loss's statistics
+    N, V, d = (1 << 22) + 5, 1 << 18, 16
+    x, w, t = ce_inputs(N, V, d)
+    assert g.linear_ce_workspace_bytes(N, V, d, g.DTYPE_BF16, 0) > 8 << 31
+    lse = ce_forward(g, x, w, t)[2]
+    for r in (slice(0, 100), slice(N - 100, N)):
+        want = torch.logsumexp(x[r].double() @ w.double().T, 1)
+        assert ((lse[r].double() - want).abs() <= 1e-5 * want).all()
+    assert g.ngram_sync_status() == g.GPT_OK
